@@ -8,7 +8,8 @@ from __future__ import annotations
 
 import torch
 
-from . import attention_backward, attention_forward
+from . import attention_backward, attention_forward, qk_norm_rope_backward
+from . import qk_norm_rope as _qk_norm_rope
 
 
 class FlashAttentionFunction(torch.autograd.Function):
@@ -34,3 +35,35 @@ class FlashAttentionFunction(torch.autograd.Function):
 def flash_attention(q, k, v, causal: bool = False, scale=None, window: int = 0):
     """Differentiable exact attention through the CUDA kernels."""
     return FlashAttentionFunction.apply(q, k, v, causal, scale, window)
+
+
+class QKNormRopeFunction(torch.autograd.Function):
+    """Per-head norm and rotation of q and k (fa_qk_norm_rope).  Saves its inputs only: the gradients recompute the
+    rows' norms.  No gradient for the tables and the positions."""
+
+    @staticmethod
+    def forward(ctx, q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved):
+        ctx.save_for_backward(q, k, q_weight, k_weight, cos, sin, positions)
+        ctx.eps, ctx.interleaved = eps, interleaved
+        return _qk_norm_rope(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dq_out, dk_out):
+        q, k, q_weight, k_weight, cos, sin, positions = ctx.saved_tensors
+        grads = qk_norm_rope_backward(q, k, _rows(dq_out), _rows(dk_out), q_weight, k_weight, cos, sin, positions,
+                                      ctx.eps, ctx.interleaved)
+        return (*grads, None, None, None, None, None)
+
+
+def _rows(t):
+    """t with strides the kernels take: contiguous rows that start on 16 bytes."""
+    if t.dim() != 4:
+        return t  # refused with the other shapes
+    fits = t.stride(3) == 1 and all(s % 8 == 0 for n, s in zip(t.shape, t.stride()[:3]) if n > 1)
+    return t if fits and t.data_ptr() % 16 == 0 else t.contiguous()
+
+
+def qk_norm_rope(q, k, q_weight=None, k_weight=None, cos=None, sin=None, positions=None, eps=1e-6, interleaved=False):
+    """Differentiable qk_norm_rope: q and k of any layout (rows that the kernels cannot take as they lie are copied)."""
+    return QKNormRopeFunction.apply(_rows(q), _rows(k), q_weight, k_weight, cos, sin, positions, eps, interleaved)

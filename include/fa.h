@@ -224,6 +224,129 @@ fa_status fa_fwd_bwd_host(const void* Q, const void* K, const void* V, const voi
                           int B, int H, int Nq, int Nk, int d, int causal, int window, float scale,
                           int heads_per_chunk, void* workspace, size_t workspace_bytes, fa_stream_t stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Operators around the attention: per-head norm and rotation of queries and
+ * keys, a paged key/value cache, and attention of drafted tokens over it.  The
+ * pages have no counterpart; the common conventions above hold for all of them.
+ * Element strides (`*_strides`) are host arrays of three: between batches, heads
+ * and rows of a [B,H,N,d] array whose last dimension is contiguous; NULL means
+ * contiguous; each must be >= 0 and a multiple of 8, and the stride of a
+ * dimension of one element is not used.  Sizes as for the attention: d 32, 64 or
+ * 128, B * heads <= 65535.
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * RMS norm of every head of Q and K, then rotation by position, one launch:
+ *   y = x / sqrt(mean(x^2) + eps) * weight,  out = rotation(y)
+ *   Q, K       : in,  bf16 [B,Hq,N,d], [B,Hk,N,d] with the given strides
+ *   Qout, Kout : out, bf16, contiguous [B,Hq,N,d], [B,Hk,N,d]
+ *   q_weight, k_weight : [d], fp32, or bf16 when weight_bf16 != 0; NULL for none
+ *   cos, sin   : fp32 [table_rows, rope/2], or both NULL (norm only; then rope = 0
+ *                and positions = NULL).  16-byte aligned.
+ *   rope       : how many leading elements of a head are rotated: a multiple of 16,
+ *                16 <= rope <= d.  Element i pairs with i + rope/2, or with
+ *                interleaved != 0 element 2i with 2i + 1; a pair (a, b) becomes
+ *                (a cos - b sin, b cos + a sin).
+ *   positions  : int32 [B,N], or NULL: row n is at position n (then N <= table_rows).
+ *                A row at a negative position is padding: its output is zero.  A
+ *                position >= table_rows gives NaN in the rotated elements.
+ * Heads counts may differ and may be 0 (that tensor's pointers may then be NULL).
+ * eps must be finite and >= 0.
+ */
+fa_status fa_qk_norm_rope(const void* Q, const void* K, void* Qout, void* Kout, const long long* q_strides,
+                          const long long* k_strides, const void* q_weight, const void* k_weight, int weight_bf16,
+                          const float* cos, const float* sin, int rope, int table_rows, int interleaved,
+                          const int* positions, int B, int Hq, int Hk, int N, int d, float eps, fa_stream_t stream);
+
+/*
+ * Its gradients, from the forward's inputs and the gradients of its outputs:
+ *   dQout, dKout : in,  bf16, with their strides
+ *   dQ, dK       : out, bf16, with their strides (rows must not overlap)
+ *   dq_weight, dk_weight : out, the type of the weights, [d]; NULL where not wanted.
+ *                  Summed in fp32 in an order that only the sizes decide.  With no
+ *                  rows they are zero.
+ *   workspace    : fa_qk_norm_rope_bwd_workspace_size() bytes, 16-byte aligned, when a
+ *                  weight gradient is wanted (FA_ERR_WORKSPACE otherwise).
+ * Padding rows get a zero gradient and add nothing to the weight gradients.
+ */
+size_t fa_qk_norm_rope_bwd_workspace_size(int B, int Hq, int Hk, int N, int d);
+fa_status fa_qk_norm_rope_bwd(const void* Q, const void* K, const void* dQout, const void* dKout, void* dQ, void* dK,
+                              const long long* q_strides, const long long* k_strides, const long long* dqout_strides,
+                              const long long* dkout_strides, const long long* dq_strides,
+                              const long long* dk_strides, const void* q_weight, const void* k_weight,
+                              void* dq_weight, void* dk_weight, int weight_bf16, const float* cos, const float* sin,
+                              int rope, int table_rows, int interleaved, const int* positions, int B, int Hq, int Hk,
+                              int N, int d, float eps, void* workspace, size_t workspace_bytes, fa_stream_t stream);
+
+/* How a cache holds its rows. */
+enum {
+    FA_CACHE_BF16 = 0,  /* bf16 */
+    FA_CACHE_E4M3 = 1   /* e4m3, one power-of-two scale 2^(byte - 127) per row: the least with
+                           max |x| <= 448 * scale, at least 2^-100; magnitudes above 1.875 *
+                           2^127 are held as that; byte 255: a row that held an infinity or
+                           a NaN, which reads back as NaN */
+};
+
+/*
+ * A paged cache of keys and values in device memory the caller owns.
+ *   K, V         : [pages, Hk, page_size, d], bf16 or e4m3, 16-byte aligned
+ *   K_exp, V_exp : [pages, Hk, page_size] exponent bytes (e4m3 only)
+ *   page_size    : a power of two, 16 .. 2^20;  pages * Hk < 2^31 - 1
+ * Which pages a sequence has is in a table the calls below take: `table` int32
+ * [B, table_cols], rows table_stride elements apart; row j of sequence b is slot
+ * j % page_size of page table[b][j / page_size].  An entry outside [0, pages) is no
+ * page: what would be written there is dropped, what would be read there is not
+ * seen.  table_cols * page_size <= 2^30.
+ * `lens` is int32 [B]: rows of each sequence, new tokens included (below 0 reads as
+ * 0).  `n_new` is int32 [B] or NULL: how many of the call's T tokens sequence b
+ * really has (clamped to 0 .. T; NULL: all T); token t < n_new[b] is at position
+ * lens[b] - n_new[b] + t, and exists only if that is >= 0.
+ */
+typedef struct {
+    void *K, *V;
+    unsigned char *K_exp, *V_exp;
+    int format, pages, Hk, page_size, d;
+} fa_cache;
+
+/*
+ * Writes T new tokens of every sequence into the cache: K, V bf16 [B,Hk,T,d] with
+ * the given strides.  Every other row of the cache stays as it was.  Two tokens must
+ * not fall on the same row (pages written through two table entries).
+ */
+fa_status fa_cache_write(const fa_cache* cache, const void* K, const void* V, const long long* k_strides,
+                         const long long* v_strides, int B, int T, const int* table, int table_cols,
+                         long long table_stride, const int* lens, const int* n_new, fa_stream_t stream);
+
+/*
+ * Reads rows 0 .. N-1 of every sequence back to contiguous bf16 [B,Hk,N,d] (e4m3 rows
+ * are exact in bf16); rows at and behind lens[b], or in no page, are zero.
+ */
+fa_status fa_cache_read(const fa_cache* cache, void* K, void* V, int B, int N, const int* table, int table_cols,
+                        long long table_stride, const int* lens, fa_stream_t stream);
+
+/*
+ * Attention of T drafted tokens per sequence over the cache (T = 1: one decoded
+ * token), whose keys and values the cache already holds (fa_cache_write):
+ *   Q : in,  bf16 contiguous [B,H,T,d]; H a multiple of the cache's Hk: query head h
+ *       reads key head h / (H / Hk)
+ *   O : out, bf16 [B,H,T,d]     L : out, fp32 [B,H,T], as in fa_fwd
+ * Token t of sequence b sees row j < lens[b] if j < lens[b] - n_new[b], or if bit
+ * dj % 64 of word dj / 64 of its row of `tree` is set, dj = j - (lens[b] - n_new[b]).
+ *   tree : 64-bit words [B, T, ceil(T/64)], sequences tree_stride words apart (0: one
+ *          tree for all); NULL: token t sees tokens 0 .. t.
+ * A row that sees no key, and rows t >= n_new[b], get O = 0 and L = -infinity.
+ * Values of keys a row does not see never reach it, be they infinite or NaN.
+ *   workspace : fa_fwd_tree_workspace_size() bytes, 16-byte aligned (FA_ERR_WORKSPACE
+ *               otherwise); calls that overlap on the GPU must not share it.
+ */
+size_t fa_fwd_tree_workspace_size(int B, int H, int Hk, int T, int d);
+fa_status fa_fwd_tree(const void* Q, const fa_cache* cache, void* O, float* L, int B, int H, int T, const int* table,
+                      int table_cols, long long table_stride, const int* lens, const int* n_new,
+                      const unsigned long long* tree, long long tree_stride, float scale, void* workspace,
+                      size_t workspace_bytes, fa_stream_t stream);
+
 /* Human-readable name of a status code (static string, never NULL). */
 const char* fa_status_string(fa_status s);
 
