@@ -214,7 +214,9 @@ fa_status make_cache_view(const fa_cache* c, const int* table, int cols, long lo
   if (B > 1 && table_stride < 0) return FA_ERR_INVALID_ARG;
   const bool some = c->pages > 0 && c->Hk > 0;
   if (some && (!c->K || !c->V || !aligned(c->K, 16) || !aligned(c->V, 16))) return FA_ERR_INVALID_ARG;
-  if (some && c->format == FA_CACHE_E4M3 && (!c->K_exp || !c->V_exp)) return FA_ERR_INVALID_ARG;
+  if (some && c->format == FA_CACHE_E4M3 &&
+      (!c->K_exp || !c->V_exp || !aligned(c->K_exp, 16) || !aligned(c->V_exp, 16)))
+    return FA_ERR_INVALID_ARG;
   if (B > 0 && (!lens || (!table && cols > 0))) return FA_ERR_INVALID_ARG;
   if (!aligned(table, 4) || !aligned(lens, 4) || !aligned(n_new, 4)) return FA_ERR_INVALID_ARG;
   int shift = 0;

@@ -7,88 +7,922 @@
 //   m = max s_j,  l = sum exp(s_j - m),  O = sum exp(s_j - m) v_j / l,  L = m + ln l.
 // A row that sees no key gets O = 0 and L = -inf.
 //
-// One block per query row, one key per warp at a time, online softmax in each warp and
-// one merge at the end.
-#include <cuda_fp8.h>
-
+// The query rows of one key head (G = H / Hk heads of T tokens, contiguous in Q) are the
+// rows of one matrix product, so a key and its value are read once for all of them.
+//
+// Work.  A unit is (sequence, key head, 128-row tile of its rows); it has one tile of 128
+// keys per 128 rows of cache.  The tiles of all units in a row are cut into equal
+// runs, one per CTA, whatever the lengths are (they are only known on the device): every
+// SM reads the same amount of cache, and a single long sequence spreads over the whole
+// GPU.  A unit that lies within one CTA is finished there; the others leave partial
+// rows (O, m, l) in the workspace, at most two per CTA, which a second kernel joins.
+//
+// Rows.  The tensor-core tile has 128 rows.  With at most 32 (or 64) query rows they are
+// repeated four (two) times in it, and each 32-row group weighs only its own quarter
+// (half) of the keys, its weights for the others being zero.  So the four softmax warps
+// share a tile's exponentials even for a single query row; the groups' results are
+// joined at the end of a unit like the partial rows of different CTAs.
+//
+// Per CTA: warp 0 loads Q and a ring of K and V tiles (TMA boxes of one page each, one
+// per lane); warp 1 issues S = Q K^T, warp 2 O += P V (tcgen05, accumulators and P in
+// tensor memory); warps 4..7 run the softmax and the epilogue.  An e4m3 cache arrives in
+// a ring of its own, from which warps 8..15 write bf16 tiles for the tensor cores: value
+// and power-of-two scale make an exact bf16 number, so from there on the two formats
+// are the same.
+//
+// Keys that are not there (behind the end, in no page) are masked; their values are
+// replaced by zeros before the product, as 0 * NaN would reach every row.  An infinite or
+// NaN value of a drafted token is taken out of the product too and goes only to the
+// rows that see the token (`Poison`).
 #include <cmath>
 
 #include "cache.cuh"
+#include "fwd_softmax.cuh"
 
 namespace fa {
 
 namespace {
 
+constexpr int kMaxGrid = 152;  // CTAs at most, one per SM
+constexpr int kKeys = 128;     // keys per tile
+
+enum : int { SITE_TREE_PRODUCER = 0x501, SITE_TREE_MMA = 0x502, SITE_TREE_SOFTMAX = 0x503, SITE_TREE_CONVERT = 0x504 };
+
+// Workspace: for every unit the CTAs that hold its first and last tile, then two partial
+// slots per CTA: [rows][D] fp32 of O, then [3][rows] of m, l, l of the rounded weights.
+struct UnitInfo {
+  int first, last;
+};
+
 struct TreeArgs {
   CacheView c;
-  const __nv_bfloat16* Q;
   __nv_bfloat16* O;
   float* L;
   const unsigned long long* tree;  // [.., T, words], or null
   long long tree_stride;           // words between sequences
-  int B, H, words;
+  int B, G, R, M, words;           // R = G * T rows per key head in M tiles
+  int rows;                        // rows of a partial slot: 32, 64 or 128
   float c_log2;
+  UnitInfo* info;
+  float* part;
+  int* status;
 };
 
 template <int D, bool FP8>
-__global__ void __launch_bounds__(128) tree_rows_kernel(const __grid_constant__ TreeArgs p) {
-  constexpr int EPL = D / 32;
-  const CacheView& c = p.c;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int t = blockIdx.x, bh = blockIdx.y, b = bh / p.H, h = bh - b * p.H, hk = h / (p.H / c.Hk);
-  const size_t row = static_cast<size_t>(bh) * c.T + t;
-  const int len = t < seq_new(c, b) ? seq_len(c, b) : 0, prefix = seq_prefix(c, b);
-  float q[EPL], o[EPL] = {}, m = -INFINITY, l = 0.f;
-  for (int e = 0; e < EPL; ++e) q[e] = __bfloat162float(p.Q[row * D + e * 32 + lane]) * p.c_log2;
-  for (int j = warp; j < len; j += 4) {
-    const int dj = j - prefix;
-    if (dj >= 0) {
-      const bool seen = p.tree == nullptr
-                            ? dj <= t
-                            : p.tree[b * p.tree_stride + static_cast<size_t>(t) * p.words + dj / 64] >> (dj % 64) & 1;
-      if (!seen) continue;
+struct TCfg {
+  static constexpr int SWB = (D * 2 >= 128) ? 128 : D * 2;
+  static constexpr int CE = SWB / 2;
+  static constexpr int NCH = D / CE;
+  static constexpr int TILE = 128 * D * 2;
+  static constexpr int NSLOT = FP8 ? 3 : 5;       // bf16 tiles, K and V in turn
+  static constexpr int NRAW = FP8 ? 4 : 0;        // e4m3 tiles
+  static constexpr int RAW = 128 * D + 128;       // with the rows' exponent bytes
+  static constexpr int NSB = 3;
+  static constexpr int OFF_Q = 0;
+  static constexpr int OFF_T = TILE;
+  static constexpr int OFF_M = OFF_T + NSLOT * TILE;      // 16 KB: epilogue exchange
+  static constexpr int OFF_RAW = OFF_M + 16384;
+  static constexpr int OFF_ROWS = OFF_RAW + NRAW * RAW;   // [3][128] floats
+  static constexpr int OFF_BAR = OFF_ROWS + 3 * 128 * 4;
+  static constexpr int B_Q = 0, B_QFREE = 1, B_FULL = 2, B_EMPTY = B_FULL + NSLOT, B_RFULL = B_EMPTY + NSLOT,
+                       B_REMPTY = B_RFULL + NRAW, B_SFULL = B_REMPTY + NRAW, B_PFULL = B_SFULL + NSB,
+                       B_PFREE = B_PFULL + NSB, B_OFULL = B_PFREE + NSB, B_OFREE = B_OFULL + 1, B_MEET = B_OFREE + 1, B_SDONE = B_MEET + 1,
+                       B_PVDONE = B_SDONE + 1, NBAR = B_PVDONE + 1;
+  static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;     // 32 words
+  static constexpr int SMEM_USED = OFF_MISC + 128;
+  static constexpr int SMEM = (SMEM_USED + 1024 > 120 * 1024) ? SMEM_USED + 1024 : 120 * 1024;
+  static constexpr int TM_S0 = 0, TM_O = NSB * 128, TM_COLS = 512;
+  static constexpr int NTHREADS = FP8 ? 512 : 256;
+  static_assert(SMEM <= 232448, "shared memory budget");
+  static_assert(TM_O + D <= TM_COLS, "tensor memory budget");
+};
+
+FA_DEV int tiles_of(const CacheView& c, int b) {
+  const int n = (seq_len(c, b) + kKeys - 1) / kKeys;
+  return n < 1 ? 1 : n;  // an empty sequence passes through as one masked tile
+}
+
+// A CTA's run of tiles, unit by unit.
+struct Walk {
+  int b, hm, t0, nt;  // sequence, key head and row tile (h * M + mt), first tile, tiles of the unit
+  long long left;     // tiles of the run from here on
+  FA_DEV bool more() const { return left > 0; }
+  FA_DEV int n() const { return nt - t0 < left ? nt - t0 : static_cast<int>(left); }
+  FA_DEV void next(const CacheView& c, int hms) {
+    left -= n();
+    t0 = 0;
+    if (++hm == hms) {
+      hm = 0;
+      ++b;
+      if (left > 0) nt = tiles_of(c, b);
     }
-    const int page = page_of(c, b, j);
-    if (page < 0) continue;
-    const size_t kr = (static_cast<size_t>(page) * c.Hk + hk) * c.page + (j & (c.page - 1));
-    auto load = [&](const uint8_t* data, const uint8_t* exps, int e) -> float {
-      if constexpr (FP8) {
-        const __half_raw hr = __nv_cvt_fp8_to_halfraw(data[kr * D + e * 32 + lane], __NV_E4M3);
-        return __half2float(__half(hr)) * __int_as_float(static_cast<int>(exps[kr]) << 23);
-      } else {
-        return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(data)[kr * D + e * 32 + lane]);
-      }
-    };
-    float s = 0.f;
-    for (int e = 0; e < EPL; ++e) s = fmaf(q[e], load(c.K, c.Ke, e), s);
-    for (int k = 16; k > 0; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
-    const float mn = fmaxf(m, s);
-    const float a = m == -INFINITY ? 0.f : exp2f(m - mn), w = exp2f(s - mn);
-    l = l * a + w;
-    for (int e = 0; e < EPL; ++e) o[e] = fmaf(w, load(c.V, c.Ve, e), o[e] * a);
-    m = mn;
   }
-  __shared__ float sm[4], sl[4], so[4][D];
-  if (lane == 0) sm[warp] = m, sl[warp] = l;
-  for (int e = 0; e < EPL; ++e) so[warp][e * 32 + lane] = o[e];
+};
+
+// Exclusive prefix of one int per thread over the block; *total for all.  NT threads.
+template <int NT>
+FA_DEV long long block_prefix(long long v, long long* scratch, long long* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long x = v;
+#pragma unroll
+  for (int k = 1; k < 32; k <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, k);
+    if (lane >= k) x += y;
+  }
+  if (lane == 31) scratch[warp] = x;
   __syncthreads();
-  if (warp != 0) return;
-  const float mx = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
-  float f[4], lt = 0.f;
-  for (int w = 0; w < 4; ++w) {
-    f[w] = sm[w] == -INFINITY ? 0.f : exp2f(sm[w] - mx);
-    lt += f[w] * sl[w];
+  long long before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < NT / 32; ++w) {
+    if (w < warp) before += scratch[w];
+    all += scratch[w];
   }
-  for (int e = 0; e < EPL; ++e) {
-    float v = 0.f;
-    for (int w = 0; w < 4; ++w)
-      if (f[w] != 0.f) v += f[w] * so[w][e * 32 + lane];
-    p.O[row * D + e * 32 + lane] = __float2bfloat16_rn(lt == 0.f ? 0.f : v / lt);
+  *total = all;
+  return before + x - v;
+}
+
+// 32 bits of a token's mask from draft index d0 on (bits below index 0 and behind the
+// token's words are 0).
+FA_DEV uint32_t draft_bits(const unsigned long long* row, int words, int t, int d0) {
+  if (d0 <= -32) return 0u;
+  if (row == nullptr) {  // tokens 0 .. t
+    const int n = t - d0 + 1;  // bits d0 .. t
+    uint32_t m = n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+    if (d0 < 0) m &= 0xffffffffu << -d0;
+    return m;
   }
-  if (lane == 0) p.L[row] = lt == 0.f ? -INFINITY : (mx + log2f(lt)) * 0.6931471805599453f;
+  if (d0 < 0) return static_cast<uint32_t>(row[0]) << -d0;
+  const int w = d0 >> 6, s = d0 & 63;
+  unsigned long long v = w < words ? row[w] >> s : 0ull;
+  if (s > 32 && w + 1 < words) v |= row[w + 1] << (64 - s);
+  return static_cast<uint32_t>(v);
+}
+FA_DEV uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
+
+// Signs of infinities and NaNs (both bits) of a value row, and, in a row's thread, of all
+// the tokens the row sees.
+template <int D>
+struct Poison {
+  uint32_t pos[D / 32], neg[D / 32];
+};
+
+// e4m3 pairs to bf16 with the scale folded in: an e4m3 number's bits 4 places down in a
+// bf16 are its value times 2^-120 (subnormals too), so one multiplication by
+// 2^(120 + k), exact, gives the value times 2^k.  m2: a second power of two where
+// 120 + k passes bf16's range (k > 7), else 1.
+FA_DEV uint32_t bf16_mul2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+FA_DEV uint32_t spread_e4m3(uint32_t h) { return (h & 0x80008000u) | ((h >> 4) & 0x07f007f0u); }
+
+// Which 16-byte unit of a row the swizzle puts where: unit ^ swz_row(row).
+template <int SWB>
+FA_DEV uint32_t swz_row(int row) {
+  return SWB == 128 ? row & 7 : (row >> 1) & 3;
+}
+
+template <int D, bool FP8, int NS>
+__global__ void __launch_bounds__(TCfg<D, FP8>::NTHREADS, 1)
+    tree_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                const __grid_constant__ CUtensorMap tmV, const __grid_constant__ TreeArgs p) {
+  using C = TCfg<D, FP8>;
+  constexpr int GR = 128 / NS;  // rows of a group, and keys each group weighs
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align1024(smem_raw);
+  const uint32_t sb = smem_u32(smem);
+  auto bar = [&](int i) -> uint32_t { return sb + C::OFF_BAR + 8 * i; };
+  uint32_t* misc = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
+  volatile int* start = reinterpret_cast<volatile int*>(misc + 2);     // b, hm, t0 of the CTA's first tile
+  volatile uint32_t* bad_rows = misc + 8;                              // 4 words
+  volatile uint32_t* bad_stage = misc + 12;                            // 8 words
+  long long* scratch = reinterpret_cast<long long*>(smem + C::OFF_ROWS);
+  const Guard guard{p.status, abort_flag};
+  const CacheView& c = p.c;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int hms = c.Hk * p.M;
+
+  if (threadIdx.x == 0) {
+    mbar_init(bar(C::B_Q), 1);
+    mbar_init(bar(C::B_QFREE), 1);
+    for (int i = 0; i < C::NSLOT; ++i) {
+      mbar_init(bar(C::B_FULL + i), FP8 ? 8 : 1);
+      mbar_init(bar(C::B_EMPTY + i), 1);
+    }
+    for (int i = 0; i < C::NRAW; ++i) {
+      mbar_init(bar(C::B_RFULL + i), 1);
+      mbar_init(bar(C::B_REMPTY + i), 8);
+    }
+    for (int i = 0; i < C::NSB; ++i) {
+      mbar_init(bar(C::B_SFULL + i), 1);
+      mbar_init(bar(C::B_PFULL + i), 4);
+      mbar_init(bar(C::B_PFREE + i), 1);
+    }
+    mbar_init(bar(C::B_OFULL), 1);
+    mbar_init(bar(C::B_OFREE), 4);
+    mbar_init(bar(C::B_MEET), 4);
+    mbar_init(bar(C::B_SDONE), 1);
+    mbar_init(bar(C::B_PVDONE), 1);
+    *abort_flag = (*reinterpret_cast<volatile int*>(p.status) != 0);
+    fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(misc), C::TM_COLS);
+    tmem_relinquish();
+  }
+  pdl_wait();  // everything from here on may be an earlier kernel's output
+  // this CTA's run of tiles
+  long long lo, mine, run;
+  {
+    const int per = (p.B + C::NTHREADS - 1) / C::NTHREADS, b0 = threadIdx.x * per, b1 = min(b0 + per, p.B);
+    long long sum = 0, total = 0;
+    for (int b = b0; b < b1; ++b) sum += tiles_of(c, b);
+    const long long before = block_prefix<C::NTHREADS>(sum, scratch, &total);
+    total *= hms;
+    run = (total + gridDim.x - 1) / gridDim.x;
+    lo = run * blockIdx.x;
+    mine = total - lo < run ? total - lo : run;
+    if (mine > 0 && lo >= before * hms && lo < (before + sum) * hms) {
+      long long at = before * hms;
+      int b = b0;
+      for (;; ++b) {
+        const long long n = static_cast<long long>(tiles_of(c, b)) * hms;
+        if (lo < at + n) break;
+        at += n;
+      }
+      const int nt = tiles_of(c, b);
+      start[0] = b;
+      start[1] = static_cast<int>((lo - at) / nt);
+      start[2] = static_cast<int>((lo - at) % nt);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = misc[0];
+  const bool skip = *abort_flag != 0 || mine <= 0;
+  Walk w{0, 0, 0, 0, 0};
+  if (!skip) {
+    w.b = start[0], w.hm = start[1], w.t0 = start[2];
+    w.nt = tiles_of(c, w.b);
+    w.left = mine;
+  }
+
+  if (warp < 4) {
+    if constexpr (FP8) regs_dec<64>();
+    if (warp == 0 && !skip) {
+      // ---------------------------------------------------------------- producer (the whole warp)
+      const int rb = c.page < kKeys ? c.page : kKeys;  // rows of a box: a page, or a tile's share of one
+      const int boxes = kKeys / rb;
+      const int nowhere = c.pages * c.Hk;              // past the end: TMA fills zeros
+      const int pi = FP8 ? lane : lane / C::NCH, ch = FP8 ? 0 : lane % C::NCH;
+      const bool issues = pi < boxes;
+      bool ok = true;
+      int items = 0, seg = 0;
+      for (; ok && w.more(); ++seg) {
+        const int len = seq_len(c, w.b), h = w.hm / p.M, mt = w.hm - h * p.M;
+        const int n = w.n();
+        auto where = [&](int tile) {  // z coordinate of this lane's box
+          const int j = tile * kKeys + pi * rb;
+          const int page = issues && j < len ? page_of(c, w.b, j) : -1;
+          return page < 0 ? nowhere : page * c.Hk + h;
+        };
+        int z = where(w.t0);
+        // Q, repeated NS times: the last product with the Q before it is done
+        if (seg > 0 && !(ok = mbar_wait_warp(bar(C::B_QFREE), (seg - 1) & 1, guard, SITE_TREE_PRODUCER))) break;
+        if (lane == 0) {
+          mbar_expect_tx(bar(C::B_Q), C::TILE);
+          for (int s = 0; s < NS; ++s)
+            for (int k = 0; k < C::NCH; ++k)
+              tma_load_3d(sb + C::OFF_Q + k * 128 * C::SWB + s * GR * C::SWB, &tmQ, bar(C::B_Q), k * C::CE, mt * 128,
+                          w.b * c.Hk + h);
+        }
+        for (int j = 0; ok && j < n; ++j) {
+          const int tile = w.t0 + j;
+          const int y = (tile * kKeys + pi * rb) & (c.page - 1);
+          const int zn = j + 1 < n ? where(tile + 1) : 0;
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv, ++items) {
+            if constexpr (FP8) {
+              const int s = items % C::NRAW;
+              if (items >= C::NRAW &&
+                  !(ok = mbar_wait_warp(bar(C::B_REMPTY + s), ((items / C::NRAW) & 1) ^ 1, guard, SITE_TREE_PRODUCER)))
+                break;
+              const uint32_t dst = sb + C::OFF_RAW + s * C::RAW, exps = dst + 128 * D + pi * rb;
+              const bool there = issues && z != nowhere;
+              const int n_there = __popc(__ballot_sync(0xffffffffu, there));
+              if (issues && !there) {  // no page, no exponents: 2^-127
+                for (int k = 0; k < rb; k += 16)
+                  asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(exps + k), "r"(0u) : "memory");
+                fence_proxy_async_smem();
+              }
+              __syncwarp();
+              if (lane == 0) mbar_expect_tx(bar(C::B_RFULL + s), 128 * D + n_there * rb);
+              __syncwarp();
+              if (issues) tma_load_3d(dst + pi * rb * D, kv ? &tmV : &tmK, bar(C::B_RFULL + s), 0, y, z);
+              if (there)
+                bulk_load(exps, (kv ? c.Ve : c.Ke) + static_cast<size_t>(z) * c.page + y, rb, bar(C::B_RFULL + s));
+            } else {
+              const int s = items % C::NSLOT;
+              if (items >= C::NSLOT &&
+                  !(ok = mbar_wait_warp(bar(C::B_EMPTY + s), ((items / C::NSLOT) & 1) ^ 1, guard, SITE_TREE_PRODUCER)))
+                break;
+              if (lane == 0) mbar_expect_tx(bar(C::B_FULL + s), C::TILE);
+              __syncwarp();
+              if (issues)
+                tma_load_3d(sb + C::OFF_T + s * C::TILE + ch * 128 * C::SWB + pi * rb * C::SWB, kv ? &tmV : &tmK,
+                            bar(C::B_FULL + s), ch * C::CE, y, z);
+            }
+          }
+          z = zn;
+        }
+        w.next(c, hms);
+      }
+      if (*abort_flag && lane == 0) {
+        // gave up: let every load this warp started land before the CTA exits
+        if (seg > 0) mbar_drain(bar(C::B_Q), (seg - 1) & 1);
+        mbar_drain(bar(C::B_Q), seg & 1);
+        constexpr int NR = FP8 ? C::NRAW : C::NSLOT, B0 = FP8 ? C::B_RFULL : C::B_FULL;
+        for (int i = items > NR ? items - NR : 0; i < items; ++i) mbar_drain(bar(B0 + i % NR), (i / NR) & 1);
+      }
+    } else if (warp == 1 && lane == 0 && !skip) {
+      // ---------------------------------------------------------------- UMMA issuer: S
+      constexpr uint32_t idS = idesc_bf16(128, kKeys, false, false);
+      bool ok = true;
+      int gs = 0, seg = 0;
+      for (; ok && w.more(); ++seg) {
+        const int n = w.n();
+        if (!(ok = mbar_wait(bar(C::B_Q), seg & 1, guard, SITE_TREE_MMA))) break;
+        for (int j = 0; j < n; ++j, ++gs) {
+          const int b = gs % C::NSB, it = 2 * gs, s = it % C::NSLOT;
+          // S buffer b last held P of tile gs-3: the product that read it is done
+          if (gs >= C::NSB && !(ok = mbar_wait(bar(C::B_PFREE + b), ((gs / C::NSB) & 1) ^ 1, guard, SITE_TREE_MMA))) break;
+          if (!(ok = mbar_wait(bar(C::B_FULL + s), (it / C::NSLOT) & 1, guard, SITE_TREE_MMA))) break;
+          tc_fence_after();
+          const uint32_t kb = sb + C::OFF_T + s * C::TILE;
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks)
+            mma_ss(tmem + C::TM_S0 + b * 128, sdesc_kmajor<C::SWB, 128>(sb + C::OFF_Q, ks),
+                   sdesc_kmajor<C::SWB, 128>(kb, ks), idS, ks > 0);
+          mma_commit(bar(C::B_SFULL + b));
+          mma_commit(bar(C::B_EMPTY + s));
+        }
+        if (!ok) break;
+        mma_commit(bar(C::B_QFREE));
+        w.next(c, hms);
+      }
+      mma_commit(bar(C::B_SDONE));  // drain point for teardown
+    } else if (warp == 2 && lane == 0 && !skip) {
+      // ---------------------------------------------------------------- UMMA issuer: P V
+      constexpr uint32_t idO = idesc_bf16(128, D, false, true);
+      bool ok = true;
+      int gs = 0, seg = 0;
+      for (; ok && w.more(); ++seg) {
+        const int n = w.n();
+        for (int j = 0; j < n; ++j, ++gs) {
+          const int b = gs % C::NSB, it = 2 * gs + 1, s = it % C::NSLOT;
+          if (!(ok = mbar_wait(bar(C::B_PFULL + b), (gs / C::NSB) & 1, guard, SITE_TREE_MMA))) break;
+          if (!(ok = mbar_wait(bar(C::B_FULL + s), (it / C::NSLOT) & 1, guard, SITE_TREE_MMA))) break;
+          // a unit's first product overwrites O: the epilogue before it has read it
+          if (j == 0 && seg > 0 && !(ok = mbar_wait(bar(C::B_OFREE), (seg - 1) & 1, guard, SITE_TREE_MMA))) break;
+          tc_fence_after();
+          const uint32_t vb = sb + C::OFF_T + s * C::TILE, aP = tmem + C::TM_S0 + b * 128;
+#pragma unroll
+          for (int ks = 0; ks < kKeys / 16; ++ks)
+            mma_ts(tmem + C::TM_O, aP + ks * 8, sdesc_mnmajor<C::SWB, 128>(vb, ks), idO, (j > 0 || ks > 0));
+          mma_commit(bar(C::B_EMPTY + s));
+          mma_commit(bar(C::B_PFREE + b));
+        }
+        if (!ok) break;
+        mma_commit(bar(C::B_OFULL));
+        w.next(c, hms);
+      }
+      mma_commit(bar(C::B_PVDONE));  // every S completed before its P: the end of all UMMAs
+    }
+  } else if (warp < 8) {
+    if constexpr (FP8) regs_inc<208>();
+    if (!skip) {
+      // ---------------------------------------------------------------- softmax + epilogue
+      const int wq = warp & 3, row = wq * 32 + lane;
+      const int group = row / GR, r_in = row % GR;  // key group, row of the query tile
+      const uint32_t tl = tmem + (static_cast<uint32_t>(wq * 32) << 16);
+      const int tid = threadIdx.x - 128;
+      float* rows = reinterpret_cast<float*>(smem + C::OFF_ROWS);
+      float4* xch = reinterpret_cast<float4*>(smem + C::OFF_M);
+      const int boxes = c.page < kKeys ? kKeys / c.page : 1;
+      bool ok = true;
+      int gs = 0, seg = 0;
+      uint32_t meet_parity = 0;
+      // the four softmax warps meet; a wait with a limit like every other
+      auto meet = [&]() -> bool {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(C::B_MEET));
+        const bool all = mbar_wait_warp(bar(C::B_MEET), meet_parity, guard, SITE_TREE_SOFTMAX);
+        meet_parity ^= 1;
+        return all;
+      };
+      for (; ok && w.more(); ++seg) {
+        const int n = w.n();
+        const int h = w.hm / p.M, mt = w.hm - h * p.M;
+        const int q = mt * 128 + r_in, t = q % c.T;
+        const int len = seq_len(c, w.b), nn = seq_new(c, w.b), prefix = seq_prefix(c, w.b);
+        const bool live = q < p.R && t < nn;  // rows that are not there see nothing
+        const bool warp_live = mt * 128 + (wq * 32) % GR < p.R;
+        const unsigned long long* trow =
+            p.tree == nullptr ? nullptr : p.tree + w.b * p.tree_stride + static_cast<size_t>(t) * p.words;
+        SoftmaxRow st;
+        Poison<D> poison;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) poison.pos[i] = poison.neg[i] = 0u;
+        auto pages_there = [&](int tile) {  // bit i: box i's page exists (this lane's load, for the ballot)
+          const int j = tile * kKeys + lane * (kKeys / boxes);
+          return lane < boxes && j < len && page_of(c, w.b, j) >= 0;
+        };
+        bool there = pages_there(w.t0);
+        for (int j = 0; j < n; ++j, ++gs) {
+          const int b = gs % C::NSB, k0 = (w.t0 + j) * kKeys;
+          const uint32_t pm = __ballot_sync(0xffffffffu, there);
+          if (j + 1 < n) there = pages_there(w.t0 + j + 1);
+          const int inside = min(prefix, len);  // keys below it are seen by every live row
+          const bool edge = k0 + kKeys > inside || pm != (boxes == 1 ? 1u : (1u << boxes) - 1u);
+          if (!(ok = mbar_wait_warp(bar(C::B_SFULL + b), (gs / C::NSB) & 1, guard, SITE_TREE_SOFTMAX))) break;
+          tc_fence_after();
+          uint32_t seen[GR / 32];  // this row's keys of its group, 32 a word
+          if (edge) {
+#pragma unroll
+            for (int i = 0; i < GR / 32; ++i) {
+              const int j0 = k0 + group * GR + 32 * i;
+              uint32_t m = low_bits(inside - j0);
+              if (j0 + 32 > prefix) m |= draft_bits(trow, p.words, t, j0 - prefix);
+              m &= low_bits(len - j0);
+              if (boxes == 8) {  // pages of 16
+                const int bx = (group * GR + 32 * i) / 16;
+                m &= ((pm >> bx) & 1u ? 0xffffu : 0u) | ((pm >> (bx + 1)) & 1u ? 0xffff0000u : 0u);
+              } else if (!((pm >> ((group * GR + 32 * i) * boxes / kKeys)) & 1u)) {
+                m = 0u;
+              }
+              seen[i] = live ? m : 0u;
+            }
+          }
+          if (k0 + kKeys > inside) {
+            // the tile holds drafted tokens or rows behind the end
+            const int it = 2 * gs + 1, s = it % C::NSLOT;
+            if (!(ok = mbar_wait_warp(bar(C::B_FULL + s), (it / C::NSLOT) & 1, guard, SITE_TREE_SOFTMAX))) break;
+            const uint32_t vb = sb + C::OFF_T + s * C::TILE;
+            const int key = k0 + row;  // this thread looks after one value row
+            uint32_t vpos[D / 32], vneg[D / 32];
+            bool bad = false;
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) vpos[i] = vneg[i] = 0u;
+            if (key >= inside) {
+              // a single token sees itself (or nothing at all): its values need no look
+              const bool look = key < len && !(c.T == 1 && p.tree == nullptr);
+#pragma unroll
+              for (int u = 0; u < D / 8; ++u) {
+                const uint32_t at = vb + (u * 8 / C::CE) * (128 * C::SWB) + row * C::SWB +
+                                    (((u * 8 % C::CE / 8) ^ swz_row<C::SWB>(row)) << 4);
+                if (key >= len) {
+                  asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0u) : "memory");
+                } else if (look) {
+                  uint32_t x[4];
+                  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                               : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                               : "r"(at)
+                               : "memory");
+                  bool here = false;
+#pragma unroll
+                  for (int e = 0; e < 8; ++e) {
+                    const uint32_t half = x[e / 2] >> (16 * (e & 1)) & 0xffffu;
+                    if ((half & 0x7f80u) == 0x7f80u) {
+                      here = true;
+                      const bool nan = (half & 0x7fu) != 0;
+                      const uint32_t bit = 1u << ((u * 8 + e) & 31);
+                      if (nan || !(half >> 15)) vpos[u / 4] |= bit;
+                      if (nan || half >> 15) vneg[u / 4] |= bit;
+                      x[e / 2] &= ~(0xffffu << (16 * (e & 1)));
+                    }
+                  }
+                  if (here) {
+                    bad = true;
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x[0]), "r"(x[1]), "r"(x[2]),
+                                 "r"(x[3])
+                                 : "memory");
+                  }
+                }
+              }
+              fence_proxy_async_smem();  // the product reads what was written here
+            }
+            const uint32_t badw = __ballot_sync(0xffffffffu, bad);
+            if (lane == 0) bad_rows[wq] = badw;
+            if (!(ok = meet())) break;
+            uint32_t bw[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) bw[i] = bad_rows[i];
+            if ((bw[0] | bw[1] | bw[2] | bw[3]) != 0) {  // hand each such row to the rows that see it
+#pragma unroll 1
+              for (int i = 0; ok && i < 128; ++i) {
+                if (!((bw[i >> 5] >> (i & 31)) & 1u)) continue;
+                if (row == i) {
+#pragma unroll
+                  for (int e = 0; e < D / 32; ++e) {
+                    bad_stage[e] = vpos[e];
+                    bad_stage[4 + e] = vneg[e];
+                  }
+                }
+                if (!(ok = meet())) break;
+                const int k = i - group * GR;
+                bool sees = false;
+#pragma unroll
+                for (int e = 0; e < GR / 32; ++e)
+                  if (k >= 32 * e && k < 32 * e + 32) sees = seen[e] >> (k & 31) & 1u;
+                if (sees) {
+#pragma unroll
+                  for (int e = 0; e < D / 32; ++e) {
+                    poison.pos[e] |= bad_stage[e];
+                    poison.neg[e] |= bad_stage[4 + e];
+                  }
+                }
+                ok = meet();
+              }
+            }
+            if (!ok || !(ok = meet())) break;  // bad_rows may be written again
+          }
+          if (warp_live) {
+            float s[GR];
+            {
+              uint32_t r[GR];
+#pragma unroll
+              for (int i = 0; i < GR / 32; ++i) tmem_ld32(tl + C::TM_S0 + b * 128 + group * GR + 32 * i, r + 32 * i);
+              tmem_ld_wait<GR>(r);
+#pragma unroll
+              for (int k = 0; k < GR; ++k) s[k] = __uint_as_float(r[k]);
+            }
+            if (edge) {
+#pragma unroll
+              for (int k = 0; k < GR; ++k)
+                if (!((seen[k / 32] >> (k & 31)) & 1u)) s[k] = -INFINITY;
+            }
+            float m4[4];
+#pragma unroll
+            for (int a = 0; a < 4; ++a) {
+              constexpr int Q4 = GR / 4;
+              m4[a] = fmaxf(s[a * Q4], s[a * Q4 + 1]);
+#pragma unroll
+              for (int k = 2; k < Q4; k += 2) m4[a] = fmax3(m4[a], s[a * Q4 + k], s[a * Q4 + k + 1]);
+            }
+            const float m_tile = fmaxf(fmax3(m4[0], m4[1], m4[2]), m4[3]) * p.c_log2;
+            if (j == 0) {
+              st.m_run = m_tile + kFwdMaxHeadroom;
+            } else {
+              const bool move = m_tile > st.m_run + kFwdRescaleThreshold;
+              if (__any_sync(0xffffffffu, move)) {
+                const float m_new = m_tile + kFwdMaxHeadroom;
+                const float alpha = move ? ex2(st.m_run - m_new) : 1.f;
+                if (move) {
+                  st.l_run *= alpha;
+                  st.lr_run *= alpha;
+                  st.m_run = m_new;
+                }
+                // the product that last wrote O is done
+                if (!(ok = mbar_wait_warp(bar(C::B_PFREE + (gs - 1) % C::NSB), ((gs - 1) / C::NSB) & 1, guard,
+                                          SITE_TREE_SOFTMAX)))
+                  break;
+                tc_fence_after();
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) {
+                  uint32_t o[32];
+                  tmem_ld32(tl + C::TM_O + 32 * i, o);
+                  tmem_ld_wait<32>(o);
+#pragma unroll
+                  for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                  tmem_st32(tl + C::TM_O + 32 * i, o);
+                }
+                tmem_st_wait();
+              }
+            }
+            const float neg_m = st.m_run == -INFINITY ? 0.f : -st.m_run;  // nothing seen so far: P = 0
+            const uint64_t cc2 = f2pack(p.c_log2, p.c_log2), nm2 = f2pack(neg_m, neg_m);
+            uint64_t ls[2] = {f2pack(0.f, 0.f), f2pack(0.f, 0.f)};
+            float rl[2] = {0.f, 0.f}, rh[2] = {0.f, 0.f};
+            uint32_t pk[GR / 2];
+#pragma unroll
+            for (int k = 0; k < GR; k += 2) {
+              float t0, t1;
+              f2unpack(ffma2(f2pack(s[k], s[k + 1]), cc2, nm2), t0, t1);
+              const float p0 = ex2(t0), p1 = ex2(t1);
+              ls[(k >> 1) & 1] = fadd2(ls[(k >> 1) & 1], f2pack(p0, p1));
+              const uint32_t v = pack_bf16x2(p0, p1);
+              pk[k >> 1] = v;
+              add_bf16x2_f32(v, rl[(k >> 1) & 1], rh[(k >> 1) & 1]);
+            }
+            float a0, a1;
+            f2unpack(fadd2(ls[0], ls[1]), a0, a1);
+            st.l_run += a0 + a1;
+            st.lr_run += (rl[0] + rl[1]) + (rh[0] + rh[1]);
+            // own keys' weights, zeros for the other groups'
+            if constexpr (NS == 1) {
+              tmem_st32(tl + C::TM_S0 + b * 128, pk);
+              tmem_st32(tl + C::TM_S0 + b * 128 + 32, pk + 32);
+            } else {
+              uint32_t zero[GR / 2];
+#pragma unroll
+              for (int k = 0; k < GR / 2; ++k) zero[k] = 0u;
+#pragma unroll
+              for (int g = 0; g < NS; ++g) {
+                const uint32_t at = tl + C::TM_S0 + b * 128 + g * (GR / 2);
+                if constexpr (NS == 2) tmem_st32(at, g == group ? pk : zero);
+                else tmem_st16(at, g == group ? pk : zero);
+              }
+            }
+            tmem_st_wait();
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(C::B_PFULL + b));
+        }
+        if (!ok) break;
+        // ------------------------------------------------------------ this run's part of the unit is done
+        if (!(ok = mbar_wait_warp(bar(C::B_OFULL), seg & 1, guard, SITE_TREE_SOFTMAX))) break;
+        tc_fence_after();
+        const bool whole = w.t0 == 0 && n == w.nt;
+        const long long unit = static_cast<long long>(w.b) * hms + w.hm;
+        if (w.t0 == 0 && tid == 0) {
+          const long long at = lo + mine - w.left;  // the unit's first tile among all tiles
+          p.info[unit] = UnitInfo{static_cast<int>(blockIdx.x), static_cast<int>((at + w.nt - 1) / run)};
+        }
+        // a NaN score does not move the maximum: where nothing else is seen it is still -inf
+        if (st.lr_run != st.lr_run) st.m_run = st.lr_run;
+        if (!live) st = SoftmaxRow();  // whatever its lane computed
+        rows[row] = st.m_run;
+        rows[128 + row] = st.l_run;
+        rows[256 + row] = st.lr_run;
+        if (!(ok = meet())) break;
+        // the groups' common reference and sums
+        float mx = -INFINITY;
+#pragma unroll
+        for (int g = 0; g < NS; ++g) mx = fmaxf(mx, rows[g * GR + r_in]);
+        const float f = st.m_run == -INFINITY ? 0.f : ex2(st.m_run - mx);
+        // the row this thread stores its share of
+        constexpr int TPR = NS, CPT = 8 / NS;  // threads per stored row; 16-byte pieces of 32 columns each
+        const int orow = tid / TPR, opart = tid % TPR;
+        float om = -INFINITY, ol = 0.f, olr = 0.f;
+#pragma unroll
+        for (int g = 0; g < NS; ++g) om = fmaxf(om, rows[g * GR + orow]);
+#pragma unroll
+        for (int g = 0; g < NS; ++g) {
+          const float mg = rows[g * GR + orow];
+          const float fg = mg == -INFINITY ? 0.f : ex2(mg - om);
+          ol += fg * rows[128 + g * GR + orow];
+          olr += fg * rows[256 + g * GR + orow];
+        }
+        if (olr != olr) om = olr;  // so that the join keeps the row
+        const int oq = mt * 128 + orow;
+        const bool store = oq < p.R;
+        const size_t grow = (static_cast<size_t>(w.b) * c.Hk + h) * p.R + oq;
+        float* slot = p.part + (2 * static_cast<size_t>(blockIdx.x) + (w.t0 == 0 ? 1 : 0)) * p.rows * (D + 3);
+        const float inv = olr == 0.f ? 0.f : 1.f / olr;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          if (!ok) continue;
+          uint32_t o[32];
+          tmem_ld32(tl + C::TM_O + 32 * i, o);
+          tmem_ld_wait<32>(o);
+          if (poison.pos[i] | poison.neg[i]) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const bool a = poison.pos[i] >> e & 1u, d = poison.neg[i] >> e & 1u;
+              if (a || d)
+                o[e] = __float_as_uint(__uint_as_float(o[e]) +
+                                       (a && d ? __int_as_float(0x7fffffff) : a ? INFINITY : -INFINITY));
+            }
+          }
+          if (i > 0 && !(ok = meet())) continue;  // the piece before has been read
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            float4 v;
+            v.x = f == 0.f ? 0.f : __uint_as_float(o[4 * k]) * f;
+            v.y = f == 0.f ? 0.f : __uint_as_float(o[4 * k + 1]) * f;
+            v.z = f == 0.f ? 0.f : __uint_as_float(o[4 * k + 2]) * f;
+            v.w = f == 0.f ? 0.f : __uint_as_float(o[4 * k + 3]) * f;
+            xch[row * 8 + (k ^ (row & 7))] = v;
+          }
+          if (!(ok = meet())) continue;
+          float a[4 * CPT];
+#pragma unroll
+          for (int k = 0; k < CPT; ++k) {
+            const int piece = opart * CPT + k;
+            float4 v = xch[orow * 8 + (piece ^ (orow & 7))];
+#pragma unroll
+            for (int g = 1; g < NS; ++g) {
+              const float4 y = xch[(g * GR + orow) * 8 + (piece ^ ((g * GR + orow) & 7))];
+              v.x += y.x, v.y += y.y, v.z += y.z, v.w += y.w;
+            }
+            a[4 * k] = v.x, a[4 * k + 1] = v.y, a[4 * k + 2] = v.z, a[4 * k + 3] = v.w;
+          }
+          if (store) {
+            const int col = 32 * i + opart * CPT * 4;
+            if (whole) {
+              uint4* dst = reinterpret_cast<uint4*>(p.O + grow * D + col);
+#pragma unroll
+              for (int k = 0; k < CPT / 2; ++k)
+                dst[k] = make_uint4(pack_bf16x2(a[8 * k] * inv, a[8 * k + 1] * inv),
+                                    pack_bf16x2(a[8 * k + 2] * inv, a[8 * k + 3] * inv),
+                                    pack_bf16x2(a[8 * k + 4] * inv, a[8 * k + 5] * inv),
+                                    pack_bf16x2(a[8 * k + 6] * inv, a[8 * k + 7] * inv));
+            } else {
+              float4* dst = reinterpret_cast<float4*>(slot + static_cast<size_t>(orow) * D + col);
+#pragma unroll
+              for (int k = 0; k < CPT; ++k) dst[k] = make_float4(a[4 * k], a[4 * k + 1], a[4 * k + 2], a[4 * k + 3]);
+            }
+          }
+        }
+        if (!ok) break;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(C::B_OFREE));
+        if (store && opart == 0) {
+          if (whole) {
+            p.L[grow] = olr == 0.f ? -INFINITY : (om + lg2(ol)) * kFwdLn2;
+          } else {
+            float* ml = slot + static_cast<size_t>(p.rows) * D;
+            ml[orow] = om;
+            ml[p.rows + orow] = ol;
+            ml[2 * p.rows + orow] = olr;
+          }
+        }
+        if (!(ok = meet())) break;  // rows and the exchange are free again
+        w.next(c, hms);
+      }
+    }
+  } else if constexpr (FP8) {
+    regs_dec<112>();
+    if (!skip) {
+      // ---------------------------------------------------------------- e4m3 -> bf16 tiles
+      const int tid = threadIdx.x - 256;
+      constexpr int PPR = D / 16;  // 16-byte pieces of an e4m3 row
+      bool ok = true;
+      int rs = 0, s = 0;                      // slots of the two rings
+      uint32_t rparity = 0, parity = 1;
+      // (a fresh barrier's phase of parity 1 counts as complete: the first trips do not wait)
+      for (long long left = 2 * mine; ok && left > 0; --left) {
+        if (!(ok = mbar_wait_warp(bar(C::B_RFULL + rs), rparity, guard, SITE_TREE_CONVERT))) break;
+        if (!(ok = mbar_wait_warp(bar(C::B_EMPTY + s), parity, guard, SITE_TREE_CONVERT))) break;
+        const uint8_t* raw = smem + C::OFF_RAW + rs * C::RAW;
+        const uint32_t dst = sb + C::OFF_T + s * C::TILE;
+#pragma unroll
+        for (int k = 0; k < 128 * PPR / 256; ++k) {
+          const int piece = k * 256 + tid, row = piece / PPR, sub = piece % PPR;
+          const uint4 x = *reinterpret_cast<const uint4*>(raw + piece * 16);
+          const int e = raw[128 * D + row];
+          const int e1 = e < 134 ? e : 134;
+          uint32_t m1 = static_cast<uint32_t>(e1 + 120) << 7;
+          m1 |= m1 << 16;
+          const uint32_t w4[4] = {x.x, x.y, x.z, x.w};
+          uint32_t o[8];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            o[2 * q] = bf16_mul2(spread_e4m3(__byte_perm(w4[q], 0, 0x1404)), m1);
+            o[2 * q + 1] = bf16_mul2(spread_e4m3(__byte_perm(w4[q], 0, 0x3424)), m1);
+          }
+          if (e > 134) {  // rare: rows with magnitudes above 57344, or that hold NaN
+            uint32_t m2 = e == kExpNaN ? 0x7fffu : static_cast<uint32_t>(127 + e - 134) << 7;
+            m2 |= m2 << 16;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) o[q] = bf16_mul2(o[q], m2);
+          }
+          // the row's 16-byte units 2 sub and 2 sub + 1; lanes of the upper half of a wide row
+          // write them in the other order, so that 8 lanes always hit 8 different units
+          const int flip = (sub * 2 / (C::CE / 8)) & 1;
+          const uint32_t base = dst + (sub * 16 / C::CE) * (128 * C::SWB) + row * C::SWB;
+          const int u0 = sub * 16 % C::CE / 8;
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const int half = q ^ flip;
+            const uint32_t at = base + ((static_cast<uint32_t>(u0 + half) ^ swz_row<C::SWB>(row)) << 4);
+            const uint32_t v0 = half ? o[4] : o[0], v1 = half ? o[5] : o[1], v2 = half ? o[6] : o[2],
+                           v3 = half ? o[7] : o[3];
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v0), "r"(v1), "r"(v2), "r"(v3)
+                         : "memory");
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar(C::B_FULL + s));
+          mbar_arrive(bar(C::B_REMPTY + rs));
+        }
+        if (++rs == C::NRAW) rs = 0, rparity ^= 1;
+        if (++s == C::NSLOT) s = 0, parity ^= 1;
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    if (!skip && *abort_flag) {
+      if (lane == 0) {
+        mbar_drain(bar(C::B_SDONE), 0);
+        mbar_drain(bar(C::B_PVDONE), 0);
+      }
+      __syncwarp();
+    }
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TM_COLS);
+  }
+}
+
+// Joins the partial rows of the units that several CTAs share: one warp per row.
+template <int D>
+__global__ void __launch_bounds__(128) tree_join_kernel(const __grid_constant__ TreeArgs p, int grid) {
+  pdl_wait();
+  if (*reinterpret_cast<volatile int*>(p.status) != 0) return;  // the kernel before gave up
+  const long long unit = blockIdx.x;
+  const UnitInfo u = p.info[unit];
+  if (u.last <= u.first || u.first < 0 || u.last >= grid) return;  // finished where it was computed
+  const int lane = threadIdx.x & 31;
+  const int mt = static_cast<int>(unit % p.M);
+  const int n = min(128, p.R - mt * 128);
+  const size_t slot_size = static_cast<size_t>(p.rows) * (D + 3);
+  for (int r = blockIdx.y * 4 + (threadIdx.x >> 5); r < n; r += gridDim.y * 4) {
+    float mx = -INFINITY;
+    for (int k = u.first + lane; k <= u.last; k += 32) {
+      const float* slot = p.part + (2 * static_cast<size_t>(k) + (k == u.first ? 1 : 0)) * slot_size;
+      mx = fmaxf(mx, slot[static_cast<size_t>(p.rows) * D + r]);
+    }
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, m));
+    float l = 0.f, lr = 0.f, o[D / 32] = {};
+    for (int k = u.first; k <= u.last; ++k) {
+      const float* slot = p.part + (2 * static_cast<size_t>(k) + (k == u.first ? 1 : 0)) * slot_size;
+      const float* ml = slot + static_cast<size_t>(p.rows) * D;
+      const float m = ml[r];
+      const float f = m == -INFINITY ? 0.f : ex2(m - mx);
+      if (f == 0.f) continue;
+      l = fmaf(f, ml[p.rows + r], l);
+      lr = fmaf(f, ml[2 * p.rows + r], lr);
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e) o[e] = fmaf(f, slot[static_cast<size_t>(r) * D + e * 32 + lane], o[e]);
+    }
+    const size_t grow = (unit / p.M) * p.R + mt * 128 + r;
+    const float inv = lr == 0.f ? 0.f : 1.f / lr;
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) p.O[grow * D + e * 32 + lane] = __float2bfloat16_rn(o[e] * inv);
+    if (lane == 0) p.L[grow] = lr == 0.f ? -INFINITY : (mx + lg2(l)) * kFwdLn2;
+  }
 }
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+// A cache without a page: no row sees a key.
+__global__ void __launch_bounds__(256) tree_empty_kernel(uint4* O, float* L, long long n16, long long rows) {
+  const long long at = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x, step = static_cast<long long>(gridDim.x) * 256;
+  for (long long i = at; i < n16; i += step) O[i] = make_uint4(0u, 0u, 0u, 0u);
+  for (long long i = at; i < rows; i += step) L[i] = -INFINITY;
+}
+
+int row_tiles(int R) { return (R + 127) / 128; }
+int slot_rows(int R) { return R <= 32 ? 32 : R <= 64 ? 64 : 128; }
+size_t info_bytes(long long units) { return (static_cast<size_t>(units) * sizeof(UnitInfo) + 255) / 256 * 256; }
+
+template <int D, bool FP8, int NS>
+fa_status launch_tree(const TreeArgs& p, const void* Q, int grid, cudaStream_t stream) {
+  using C = TCfg<D, FP8>;
+  const CacheView& c = p.c;
+  CUtensorMap mQ, mK, mV;
+  const int rb = c.page < kKeys ? c.page : kKeys, heads = c.pages * c.Hk;
+  if (!encode_bf16_3d(&mQ, Q, D, p.R, p.B * c.Hk, C::CE, 128 / NS)) return FA_ERR_CUDA;
+  if (FP8) {
+    if (!encode_u8_3d(&mK, c.K, D, c.page, heads, D, rb) || !encode_u8_3d(&mV, c.V, D, c.page, heads, D, rb))
+      return FA_ERR_CUDA;
+  } else {
+    if (!encode_bf16_3d(&mK, c.K, D, c.page, heads, C::CE, rb) || !encode_bf16_3d(&mV, c.V, D, c.page, heads, C::CE, rb))
+      return FA_ERR_CUDA;
+  }
+  auto kern = tree_kernel<D, FP8, NS>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
+    return FA_ERR_CUDA;
+  if (launch_pdl(kern, dim3(grid), dim3(C::NTHREADS), C::SMEM, stream, mQ, mK, mV, p) != cudaSuccess)
+    return FA_ERR_CUDA;
+  const unsigned units = static_cast<unsigned>(p.B) * c.Hk * p.M;
+  const int n = p.R < 128 ? p.R : 128;
+  const cudaError_t e = launch_pdl(tree_join_kernel<D>, dim3(units, (n + 3) / 4), dim3(128), 0, stream, p, grid);
+  return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+template <int D, bool FP8>
+fa_status launch_tree_rows(const TreeArgs& p, const void* Q, int grid, cudaStream_t s) {
+  return p.R <= 32   ? launch_tree<D, FP8, 4>(p, Q, grid, s)
+         : p.R <= 64 ? launch_tree<D, FP8, 2>(p, Q, grid, s)
+                     : launch_tree<D, FP8, 1>(p, Q, grid, s);
+}
 
 }  // namespace
 }  // namespace fa
@@ -100,7 +934,11 @@ extern "C" {
 size_t fa_fwd_tree_workspace_size(int B, int H, int Hk, int T, int d) {
   if (B < 0 || H < 0 || Hk < 0 || T < 0 || (d != 32 && d != 64 && d != 128) || (H > 0 && (Hk == 0 || H % Hk != 0)))
     return static_cast<size_t>(-1);
-  return 0;
+  if (B == 0 || H == 0 || T == 0) return 0;
+  const long long R = static_cast<long long>(H / Hk) * T;
+  if (static_cast<long long>(B) * H > 65535 || R > (1LL << 30)) return static_cast<size_t>(-1);
+  const long long units = static_cast<long long>(B) * Hk * row_tiles(static_cast<int>(R));
+  return info_bytes(units) + 2 * static_cast<size_t>(kMaxGrid) * slot_rows(static_cast<int>(R)) * (d + 3) * sizeof(float);
 }
 
 fa_status fa_fwd_tree(const void* Q, const fa_cache* cache, void* O, float* L, int B, int H, int T, const int* table,
@@ -116,30 +954,44 @@ fa_status fa_fwd_tree(const void* Q, const fa_cache* cache, void* O, float* L, i
   if (static_cast<long long>(B) * H > 65535) return FA_ERR_UNSUPPORTED;
   if (tree != nullptr && (!aligned(tree, 8) || tree_stride < 0)) return FA_ERR_INVALID_ARG;
   if (B == 0 || H == 0 || T == 0) return FA_OK;
-  if (static_cast<long long>(H / cache->Hk) * T > (1LL << 30)) return FA_ERR_UNSUPPORTED;
+  const long long R = static_cast<long long>(H / cache->Hk) * T;
+  if (R > (1LL << 30)) return FA_ERR_UNSUPPORTED;
   if (!Q || !O || !L || !aligned(Q, 16) || !aligned(O, 16) || !aligned(L, 4)) return FA_ERR_INVALID_ARG;
-  (void)workspace, (void)workspace_bytes;
-  p.Q = static_cast<const __nv_bfloat16*>(Q);
+  const size_t need = fa_fwd_tree_workspace_size(B, H, cache->Hk, T, cache->d);
+  if (workspace == nullptr || workspace_bytes < need || !aligned(workspace, 16)) return FA_ERR_WORKSPACE;
+  p.status = device_status_word();
+  if (p.status == nullptr) return FA_ERR_CUDA;
   p.O = static_cast<__nv_bfloat16*>(O);
   p.L = L;
   p.tree = tree;
   p.tree_stride = B > 1 ? tree_stride : 0;
-  p.B = B, p.H = H, p.words = (T + 63) / 64;
+  p.B = B, p.G = H / cache->Hk, p.R = static_cast<int>(R), p.M = row_tiles(p.R), p.words = (T + 63) / 64;
+  p.rows = slot_rows(p.R);
   p.c_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
-  const dim3 grid(T, B * H);
-  const bool fp8 = cache->format == FA_CACHE_E4M3;
-#define FA_TREE(D)                                                       \
-  case D:                                                                \
-    if (fp8) tree_rows_kernel<D, true><<<grid, 128, 0, stream>>>(p);     \
-    else tree_rows_kernel<D, false><<<grid, 128, 0, stream>>>(p);        \
-    break;
-  switch (cache->d) {
-    FA_TREE(32)
-    FA_TREE(64)
-    FA_TREE(128)
+  const long long units = static_cast<long long>(B) * cache->Hk * p.M;
+  if (units > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
+  p.info = static_cast<UnitInfo*>(workspace);
+  p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + info_bytes(units));
+  if (cache->pages == 0 || table_cols == 0) {
+    const long long rows = static_cast<long long>(B) * H * T;
+    tree_empty_kernel<<<kMaxGrid, 256, 0, stream>>>(static_cast<uint4*>(O), L, rows * cache->d / 8, rows);
+    return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
   }
-#undef FA_TREE
-  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  int grid = 0, dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&grid, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return FA_ERR_CUDA;
+  // no more CTAs than there can be tiles
+  const long long most = units * ((static_cast<long long>(table_cols) * cache->page_size + kKeys - 1) / kKeys);
+  if (grid > kMaxGrid) grid = kMaxGrid;
+  if (most < grid) grid = static_cast<int>(most);
+  const bool fp8 = cache->format == FA_CACHE_E4M3;
+  switch (cache->d) {
+    case 32: return fp8 ? launch_tree_rows<32, true>(p, Q, grid, stream) : launch_tree_rows<32, false>(p, Q, grid, stream);
+    case 64: return fp8 ? launch_tree_rows<64, true>(p, Q, grid, stream) : launch_tree_rows<64, false>(p, Q, grid, stream);
+    default:
+      return fp8 ? launch_tree_rows<128, true>(p, Q, grid, stream) : launch_tree_rows<128, false>(p, Q, grid, stream);
+  }
 }
 
 }  // extern "C"

@@ -111,6 +111,8 @@ int* device_status_word();
 // Encodes a 3-D bf16 tensor map over a contiguous [BH, N, d] array: dims
 // (d, N, BH), box (inner, rows, 1), swizzle width = inner * 2 bytes (<= 128).
 bool encode_bf16_3d(CUtensorMap* map, const void* base, int d, int N, int BH, int inner, int rows);
+// The same for bytes, without a swizzle.
+bool encode_u8_3d(CUtensorMap* map, const void* base, int d, int N, int BH, int inner, int rows);
 // 2-D bf16 tensor map over a row-major [rows_total][inner_total] array.
 bool encode_bf16_2d(CUtensorMap* map, const void* base, int inner_total, int rows_total, int box_inner,
                     int box_rows);

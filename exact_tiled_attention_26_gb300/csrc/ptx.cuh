@@ -121,6 +121,12 @@ FA_DEV void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int 
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
 }
+// `bytes` contiguous bytes of global memory (both 16-byte aligned, bytes a multiple of 16).
+FA_DEV void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
 // Element-wise fp32 add of `bytes` contiguous bytes of shared memory into global
 // memory (both 16-byte aligned, bytes a multiple of 16), performed in L2.
 FA_DEV void bulk_reduce_add_f32(float* gdst, uint32_t ssrc, uint32_t bytes) {

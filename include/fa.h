@@ -292,7 +292,7 @@ enum {
 /*
  * A paged cache of keys and values in device memory the caller owns.
  *   K, V         : [pages, Hk, page_size, d], bf16 or e4m3, 16-byte aligned
- *   K_exp, V_exp : [pages, Hk, page_size] exponent bytes (e4m3 only)
+ *   K_exp, V_exp : [pages, Hk, page_size] exponent bytes, 16-byte aligned (e4m3 only)
  *   page_size    : a power of two, 16 .. 2^20;  pages * Hk < 2^31 - 1
  * Which pages a sequence has is in a table the calls below take: `table` int32
  * [B, table_cols], rows table_stride elements apart; row j of sequence b is slot
