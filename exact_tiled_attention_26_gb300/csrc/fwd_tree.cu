@@ -24,16 +24,22 @@
 // joined at the end of a unit like the partial rows of different CTAs.
 //
 // Per CTA: warp 0 loads Q and a ring of K and V tiles (TMA boxes of one page each, one
-// per lane); warp 1 issues S = Q K^T, warp 2 O += P V (tcgen05, accumulators and P in
-// tensor memory); warps 4..7 run the softmax and the epilogue.  An e4m3 cache arrives in
-// a ring of its own, from which warps 8..15 write bf16 tiles for the tensor cores: value
-// and power-of-two scale make an exact bf16 number, so from there on the two formats
-// are the same.
+// per lane); warp 1 issues S = Q K^T, warp 2 O += P V (tcgen05; Q, P and the accumulators in
+// tensor memory); warps 4..7 put Q there, run the softmax and the epilogue.
+//
+// An e4m3 cache arrives in a ring of its own; warps 8..15 turn its tiles into f16 tiles
+// (one instruction for two elements, exact) and Q is scaled to f16 row by row.  The
+// power-of-two scales stay out of the products: a key's multiplies its scores, a value's
+// its weights, so that a row's weights are kept in f16's range by the largest of score +
+// exponent of the value.
 //
 // Keys that are not there (behind the end, in no page) are masked; their values are
 // replaced by zeros before the product, as 0 * NaN would reach every row.  An infinite or
 // NaN value of a drafted token is taken out of the product too and goes only to the
 // rows that see the token (`Poison`).
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
 #include <cmath>
 
 #include "cache.cuh"
@@ -74,27 +80,29 @@ struct TCfg {
   static constexpr int CE = SWB / 2;
   static constexpr int NCH = D / CE;
   static constexpr int TILE = 128 * D * 2;
-  static constexpr int NSLOT = FP8 ? 3 : 5;       // bf16 tiles, K and V in turn
-  static constexpr int NRAW = FP8 ? 4 : 0;        // e4m3 tiles
-  static constexpr int RAW = 128 * D + 128;       // with the rows' exponent bytes
-  static constexpr int NSB = 3;
-  static constexpr int OFF_Q = 0;
-  static constexpr int OFF_T = TILE;
-  static constexpr int OFF_M = OFF_T + NSLOT * TILE;      // 16 KB: epilogue exchange
-  static constexpr int OFF_RAW = OFF_M + 16384;
-  static constexpr int OFF_ROWS = OFF_RAW + NRAW * RAW;   // [3][128] floats
+  static constexpr int NSLOT = FP8 ? (D == 128 ? 4 : 6) : (D == 128 ? 6 : 8);  // 16-bit tiles, K and V in turn
+  static constexpr int NRAW = FP8 ? (D == 128 ? 3 : 6) : 0;                    // e4m3 tiles
+  static constexpr int RAW = 128 * D + 256;     // with the exponent bytes of its keys (K tiles: and of their values)
+  static constexpr int NSB = D == 128 ? 2 : 3;  // S / P buffers in tensor memory
+  static constexpr int NSC = FP8 ? NSLOT / 2 + NSB : 0;  // tiles whose scales are kept (see the converter)
+  static constexpr int OFF_T = 0;
+  static constexpr int OFF_Q = OFF_T + NSLOT * TILE;     // 128 / NS rows; the epilogue's exchange (NS > 1) behind them
+  static constexpr int OFF_RAW = OFF_Q + 32768;
+  static constexpr int OFF_SCALE = OFF_RAW + NRAW * RAW;  // [NSC][3][128] floats: 2^k of K, 2^k of V, k of V
+  static constexpr int OFF_ROWS = OFF_SCALE + NSC * 3 * 128 * 4;  // [3][128] floats
   static constexpr int OFF_BAR = OFF_ROWS + 3 * 128 * 4;
-  static constexpr int B_Q = 0, B_QFREE = 1, B_FULL = 2, B_EMPTY = B_FULL + NSLOT, B_RFULL = B_EMPTY + NSLOT,
-                       B_REMPTY = B_RFULL + NRAW, B_SFULL = B_REMPTY + NRAW, B_PFULL = B_SFULL + NSB,
-                       B_PFREE = B_PFULL + NSB, B_OFULL = B_PFREE + NSB, B_OFREE = B_OFULL + 1, B_MEET = B_OFREE + 1, B_SDONE = B_MEET + 1,
-                       B_PVDONE = B_SDONE + 1, NBAR = B_PVDONE + 1;
-  static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;     // 32 words
-  static constexpr int SMEM_USED = OFF_MISC + 128;
+  static constexpr int B_Q = 0, B_QFREE = 1, B_QREADY = 2, B_FULL = 3, B_EMPTY = B_FULL + NSLOT,
+                       B_RFULL = B_EMPTY + NSLOT, B_REMPTY = B_RFULL + NRAW, B_SFULL = B_REMPTY + NRAW,
+                       B_PFULL = B_SFULL + NSB, B_PFREE = B_PFULL + NSB, B_OFULL = B_PFREE + NSB, B_OFREE = B_OFULL + 1,
+                       B_MEET = B_OFREE + 1, B_SDONE = B_MEET + 1, B_PVDONE = B_SDONE + 1, NBAR = B_PVDONE + 1;
+  static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;     // 24 words
+  static constexpr int SMEM_USED = OFF_MISC + 96;
   static constexpr int SMEM = (SMEM_USED + 1024 > 120 * 1024) ? SMEM_USED + 1024 : 120 * 1024;
-  static constexpr int TM_S0 = 0, TM_O = NSB * 128, TM_COLS = 512;
+  // tensor memory columns: S / P buffers, O, Q (two elements a column)
+  static constexpr int TM_S0 = 0, TM_O = NSB * 128, TM_Q = TM_O + D, TM_COLS = 512;
   static constexpr int NTHREADS = FP8 ? 512 : 256;
   static_assert(SMEM <= 232448, "shared memory budget");
-  static_assert(TM_O + D <= TM_COLS, "tensor memory budget");
+  static_assert(TM_Q + D / 2 <= TM_COLS, "tensor memory budget");
 };
 
 FA_DEV int tiles_of(const CacheView& c, int b) {
@@ -166,21 +174,117 @@ struct Poison {
   uint32_t pos[D / 32], neg[D / 32];
 };
 
-// e4m3 pairs to bf16 with the scale folded in: an e4m3 number's bits 4 places down in a
-// bf16 are its value times 2^-120 (subnormals too), so one multiplication by
-// 2^(120 + k), exact, gives the value times 2^k.  m2: a second power of two where
-// 120 + k passes bf16's range (k > 7), else 1.
-FA_DEV uint32_t bf16_mul2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
+// Two e4m3 numbers as two f16 numbers, exactly.
+FA_DEV uint32_t e4m3x2_to_f16x2(uint32_t two) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two), __NV_E4M3);
+  return static_cast<uint32_t>(h.x) | static_cast<uint32_t>(h.y) << 16;
 }
-FA_DEV uint32_t spread_e4m3(uint32_t h) { return (h & 0x80008000u) | ((h >> 4) & 0x07f007f0u); }
+FA_DEV uint32_t pack_f16x2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+FA_DEV uint4 ld_shared_v4(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+  return v;
+}
+FA_DEV void st_shared_v4(uint32_t at, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+// The e4m3 format's weights are f16 numbers: 2^(score + exponent of the value - reference)
+// starts at 2^kF16Start for a row's largest and the reference moves before it passes
+// 2^kF16Top.  Whatever is 2^-18 of the largest or more keeps 11 bits.
+constexpr float kF16Start = 4.f, kF16Top = 14.f;
 
 // Which 16-byte unit of a row the swizzle puts where: unit ^ swz_row(row).
 template <int SWB>
 FA_DEV uint32_t swz_row(int row) {
   return SWB == 128 ? row & 7 : (row >> 1) & 3;
+}
+
+// Value rows of a tile that is not all prefix, looked after by the four softmax warps (one
+// row per thread, which have all met): rows behind the end become zero, as 0 * NaN would
+// reach every row of the product; infinities and NaNs of drafted tokens are taken out and
+// noted in the poison of the rows that see the token.  Loops stay loops: the code runs once
+// or twice per unit.
+template <int D, bool FP8, int GR>
+FA_DEV void clean_values(uint32_t tile, int row, int key, int inside, int len, bool look, int group,
+                         const uint32_t* seen, Poison<D>& poison, volatile uint32_t* bad_rows,
+                         volatile uint32_t* bad_stage) {
+  using C = TCfg<D, FP8>;
+  constexpr uint32_t EXP = FP8 ? 0x7c00u : 0x7f80u, MANT = FP8 ? 0x03ffu : 0x007fu;
+  const int lane = row & 31;
+  auto unit = [&](int u) {
+    return tile + (u * 8 / C::CE) * (128 * C::SWB) + row * C::SWB + (((u % (C::CE / 8)) ^ swz_row<C::SWB>(row)) << 4);
+  };
+  bool bad = false;
+  if (key >= len) {
+#pragma unroll 1
+    for (int u = 0; u < D / 8; ++u) st_shared_v4(unit(u), make_uint4(0u, 0u, 0u, 0u));
+  } else if (key >= inside && look) {
+#pragma unroll 1
+    for (int u = 0; u < D / 8; ++u) {
+      const uint4 v = ld_shared_v4(unit(u));
+      const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) bad |= (x[e] & EXP) == EXP || (x[e] & EXP << 16) == EXP << 16;
+    }
+  }
+  const uint32_t badw = __ballot_sync(0xffffffffu, bad);
+  if (lane == 0) bad_rows[row >> 5] = badw;
+  if (key >= inside) fence_proxy_async_smem();  // the product reads what was written here
+  named_bar_sync(1, 128);
+#pragma unroll 1
+  for (int i = 0; i < 128; ++i) {
+    const uint32_t word = bad_rows[i >> 5];
+    if (word == 0) {
+      i |= 31;
+      continue;
+    }
+    if (!((word >> (i & 31)) & 1u)) continue;
+    // row i's infinities and NaNs: out of the tile, into bad_stage, to the rows that see it
+    if (row == i) {
+#pragma unroll 1
+      for (int k = 0; k < D / 32; ++k) {
+        uint32_t pos = 0, neg = 0;
+#pragma unroll 1
+        for (int u = 4 * k; u < 4 * k + 4; ++u) {
+          const uint4 v = ld_shared_v4(unit(u));
+          uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const uint32_t half = x[e / 2] >> (16 * (e & 1)) & 0xffffu;
+            if ((half & EXP) == EXP) {
+              const bool nan = (half & MANT) != 0;
+              const uint32_t bit = 1u << ((u & 3) * 8 + e);
+              if (nan || !(half >> 15)) pos |= bit;
+              if (nan || half >> 15) neg |= bit;
+              x[e / 2] &= ~(0xffffu << (16 * (e & 1)));
+            }
+          }
+          st_shared_v4(unit(u), make_uint4(x[0], x[1], x[2], x[3]));
+        }
+        bad_stage[k] = pos;
+        bad_stage[4 + k] = neg;
+      }
+      fence_proxy_async_smem();
+    }
+    named_bar_sync(1, 128);
+    const int k = i - group * GR;
+    bool sees = false;
+#pragma unroll
+    for (int e = 0; e < GR / 32; ++e)
+      if (k >= 32 * e && k < 32 * e + 32) sees = seen[e] >> (k & 31) & 1u;
+    if (sees) {
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e) {
+        poison.pos[e] |= bad_stage[e];
+        poison.neg[e] |= bad_stage[4 + e];
+      }
+    }
+    named_bar_sync(1, 128);
+  }
+  named_bar_sync(1, 128);  // bad_rows may be written again
 }
 
 template <int D, bool FP8, int NS>
@@ -195,25 +299,27 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::NTHREADS, 1)
   auto bar = [&](int i) -> uint32_t { return sb + C::OFF_BAR + 8 * i; };
   uint32_t* misc = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
-  volatile int* start = reinterpret_cast<volatile int*>(misc + 2);     // b, hm, t0 of the CTA's first tile
-  volatile uint32_t* bad_rows = misc + 8;                              // 4 words
-  volatile uint32_t* bad_stage = misc + 12;                            // 8 words
+  volatile int* start = reinterpret_cast<volatile int*>(misc + 2);  // b, hm, t0 of the CTA's first tile
+  volatile uint32_t* bad_rows = misc + 8;                           // 4 words
+  volatile uint32_t* bad_stage = misc + 12;                         // 8 words
   long long* scratch = reinterpret_cast<long long*>(smem + C::OFF_ROWS);
   const Guard guard{p.status, abort_flag};
   const CacheView& c = p.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int hms = c.Hk * p.M;
 
+  pdl_trigger();  // the joining kernel may be made ready now; it waits for this one's end
   if (threadIdx.x == 0) {
     mbar_init(bar(C::B_Q), 1);
-    mbar_init(bar(C::B_QFREE), 1);
+    mbar_init(bar(C::B_QFREE), 4);
+    mbar_init(bar(C::B_QREADY), 4);
     for (int i = 0; i < C::NSLOT; ++i) {
-      mbar_init(bar(C::B_FULL + i), FP8 ? 8 : 1);
+      mbar_init(bar(C::B_FULL + i), FP8 ? 4 : 1);
       mbar_init(bar(C::B_EMPTY + i), 1);
     }
     for (int i = 0; i < C::NRAW; ++i) {
       mbar_init(bar(C::B_RFULL + i), 1);
-      mbar_init(bar(C::B_REMPTY + i), 8);
+      mbar_init(bar(C::B_REMPTY + i), 4);
     }
     for (int i = 0; i < C::NSB; ++i) {
       mbar_init(bar(C::B_SFULL + i), 1);
@@ -225,19 +331,14 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::NTHREADS, 1)
     mbar_init(bar(C::B_MEET), 4);
     mbar_init(bar(C::B_SDONE), 1);
     mbar_init(bar(C::B_PVDONE), 1);
-    *abort_flag = (*reinterpret_cast<volatile int*>(p.status) != 0);
     fence_mbar_init();
-  }
-  if (warp == 0 && lane == 0) {
-    tma_prefetch_desc(&tmQ);
-    tma_prefetch_desc(&tmK);
-    tma_prefetch_desc(&tmV);
   }
   if (warp == 1) {
     tmem_alloc(smem_u32(misc), C::TM_COLS);
     tmem_relinquish();
   }
   pdl_wait();  // everything from here on may be an earlier kernel's output
+  if (threadIdx.x == 64) *abort_flag = (*reinterpret_cast<volatile int*>(p.status) != 0);
   // this CTA's run of tiles
   long long lo, mine, run;
   {
@@ -276,7 +377,7 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::NTHREADS, 1)
   }
 
   if (warp < 4) {
-    if constexpr (FP8) regs_dec<64>();
+    if constexpr (FP8) regs_dec<80>();
     if (warp == 0 && !skip) {
       // ---------------------------------------------------------------- producer (the whole warp)
       const int rb = c.page < kKeys ? c.page : kKeys;  // rows of a box: a page, or a tile's share of one
@@ -285,7 +386,10 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::NTHREADS, 1)
       const int pi = FP8 ? lane : lane / C::NCH, ch = FP8 ? 0 : lane % C::NCH;
       const bool issues = pi < boxes;
       bool ok = true;
-      int items = 0, seg = 0;
+      int items = 0, seg = 0, slot = 0;
+      uint32_t parity = 1;  // (a fresh barrier's phase of parity 1 counts as complete: the first trips do not wait)
+      constexpr int NR = FP8 ? C::NRAW : C::NSLOT, BFULL = FP8 ? C::B_RFULL : C::B_FULL,
+                    BEMPTY = FP8 ? C::B_REMPTY : C::B_EMPTY;
       for (; ok && w.more(); ++seg) {
         const int len = seq_len(c, w.b), h = w.hm / p.M, mt = w.hm - h * p.M;
         const int n = w.n();
@@ -295,51 +399,48 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::NTHREADS, 1)
           return page < 0 ? nowhere : page * c.Hk + h;
         };
         int z = where(w.t0);
-        // Q, repeated NS times: the last product with the Q before it is done
+        // the softmax warps have taken the Q before it
         if (seg > 0 && !(ok = mbar_wait_warp(bar(C::B_QFREE), (seg - 1) & 1, guard, SITE_TREE_PRODUCER))) break;
         if (lane == 0) {
-          mbar_expect_tx(bar(C::B_Q), C::TILE);
-          for (int s = 0; s < NS; ++s)
-            for (int k = 0; k < C::NCH; ++k)
-              tma_load_3d(sb + C::OFF_Q + k * 128 * C::SWB + s * GR * C::SWB, &tmQ, bar(C::B_Q), k * C::CE, mt * 128,
-                          w.b * c.Hk + h);
+          mbar_expect_tx(bar(C::B_Q), GR * D * 2);
+          for (int k = 0; k < C::NCH; ++k)
+            tma_load_3d(sb + C::OFF_Q + k * GR * C::SWB, &tmQ, bar(C::B_Q), k * C::CE, mt * 128, w.b * c.Hk + h);
         }
         for (int j = 0; ok && j < n; ++j) {
           const int tile = w.t0 + j;
           const int y = (tile * kKeys + pi * rb) & (c.page - 1);
           const int zn = j + 1 < n ? where(tile + 1) : 0;
-#pragma unroll
-          for (int kv = 0; kv < 2; ++kv, ++items) {
+          for (int kv = 0; kv < 2; ++kv) {
+            if (!(ok = mbar_wait_warp(bar(BEMPTY + slot), parity, guard, SITE_TREE_PRODUCER))) break;
+            const uint32_t full = bar(BFULL + slot);
             if constexpr (FP8) {
-              const int s = items % C::NRAW;
-              if (items >= C::NRAW &&
-                  !(ok = mbar_wait_warp(bar(C::B_REMPTY + s), ((items / C::NRAW) & 1) ^ 1, guard, SITE_TREE_PRODUCER)))
-                break;
-              const uint32_t dst = sb + C::OFF_RAW + s * C::RAW, exps = dst + 128 * D + pi * rb;
+              const uint32_t dst = sb + C::OFF_RAW + slot * C::RAW, exps = dst + 128 * D + pi * rb;
               const bool there = issues && z != nowhere;
               const int n_there = __popc(__ballot_sync(0xffffffffu, there));
-              if (issues && !there) {  // no page, no exponents: 2^-127
-                for (int k = 0; k < rb; k += 16)
-                  asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(exps + k), "r"(0u) : "memory");
+              if (kv == 0 && issues && !there) {  // no page, no exponents: 2^-127
+                for (int k = 0; k < rb; k += 16) {
+                  st_shared_v4(exps + k, make_uint4(0u, 0u, 0u, 0u));
+                  st_shared_v4(exps + 128 + k, make_uint4(0u, 0u, 0u, 0u));
+                }
                 fence_proxy_async_smem();
               }
               __syncwarp();
-              if (lane == 0) mbar_expect_tx(bar(C::B_RFULL + s), 128 * D + n_there * rb);
+              if (lane == 0) mbar_expect_tx(full, 128 * D + (kv == 0 ? 2 * n_there * rb : 0));
               __syncwarp();
-              if (issues) tma_load_3d(dst + pi * rb * D, kv ? &tmV : &tmK, bar(C::B_RFULL + s), 0, y, z);
-              if (there)
-                bulk_load(exps, (kv ? c.Ve : c.Ke) + static_cast<size_t>(z) * c.page + y, rb, bar(C::B_RFULL + s));
+              if (issues) tma_load_3d(dst + pi * rb * D, kv ? &tmV : &tmK, full, 0, y, z);
+              if (kv == 0 && there) {
+                bulk_load(exps, c.Ke + static_cast<size_t>(z) * c.page + y, rb, full);
+                bulk_load(exps + 128, c.Ve + static_cast<size_t>(z) * c.page + y, rb, full);
+              }
             } else {
-              const int s = items % C::NSLOT;
-              if (items >= C::NSLOT &&
-                  !(ok = mbar_wait_warp(bar(C::B_EMPTY + s), ((items / C::NSLOT) & 1) ^ 1, guard, SITE_TREE_PRODUCER)))
-                break;
-              if (lane == 0) mbar_expect_tx(bar(C::B_FULL + s), C::TILE);
+              if (lane == 0) mbar_expect_tx(full, C::TILE);
               __syncwarp();
               if (issues)
-                tma_load_3d(sb + C::OFF_T + s * C::TILE + ch * 128 * C::SWB + pi * rb * C::SWB, kv ? &tmV : &tmK,
-                            bar(C::B_FULL + s), ch * C::CE, y, z);
+                tma_load_3d(sb + C::OFF_T + slot * C::TILE + ch * 128 * C::SWB + pi * rb * C::SWB, kv ? &tmV : &tmK, full,
+                            ch * C::CE, y, z);
             }
+            ++items;
+            if (++slot == NR) slot = 0, parity ^= 1;
           }
           z = zn;
         }
@@ -349,47 +450,46 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::NTHREADS, 1)
         // gave up: let every load this warp started land before the CTA exits
         if (seg > 0) mbar_drain(bar(C::B_Q), (seg - 1) & 1);
         mbar_drain(bar(C::B_Q), seg & 1);
-        constexpr int NR = FP8 ? C::NRAW : C::NSLOT, B0 = FP8 ? C::B_RFULL : C::B_FULL;
-        for (int i = items > NR ? items - NR : 0; i < items; ++i) mbar_drain(bar(B0 + i % NR), (i / NR) & 1);
+        for (int i = items > NR ? items - NR : 0; i < items; ++i) mbar_drain(bar(BFULL + i % NR), (i / NR) & 1);
       }
     } else if (warp == 1 && lane == 0 && !skip) {
-      // ---------------------------------------------------------------- UMMA issuer: S
-      constexpr uint32_t idS = idesc_bf16(128, kKeys, false, false);
+      // ---------------------------------------------------------------- UMMA issuer: S = Q (tensor memory) x K
+      constexpr uint32_t idS = FP8 ? idesc_f16(128, kKeys, false, false) : idesc_bf16(128, kKeys, false, false);
       bool ok = true;
-      int gs = 0, seg = 0;
+      int seg = 0, b = 0, s = 0;
+      uint32_t bpar = 1, spar = 0;
       for (; ok && w.more(); ++seg) {
         const int n = w.n();
-        if (!(ok = mbar_wait(bar(C::B_Q), seg & 1, guard, SITE_TREE_MMA))) break;
-        for (int j = 0; j < n; ++j, ++gs) {
-          const int b = gs % C::NSB, it = 2 * gs, s = it % C::NSLOT;
-          // S buffer b last held P of tile gs-3: the product that read it is done
-          if (gs >= C::NSB && !(ok = mbar_wait(bar(C::B_PFREE + b), ((gs / C::NSB) & 1) ^ 1, guard, SITE_TREE_MMA))) break;
-          if (!(ok = mbar_wait(bar(C::B_FULL + s), (it / C::NSLOT) & 1, guard, SITE_TREE_MMA))) break;
+        if (!(ok = mbar_wait(bar(C::B_QREADY), seg & 1, guard, SITE_TREE_MMA))) break;
+        for (int j = 0; j < n; ++j) {
+          // S buffer b last held P of an earlier tile: the product that read it is done
+          if (!(ok = mbar_wait(bar(C::B_PFREE + b), bpar, guard, SITE_TREE_MMA))) break;
+          if (!(ok = mbar_wait(bar(C::B_FULL + s), spar, guard, SITE_TREE_MMA))) break;
           tc_fence_after();
           const uint32_t kb = sb + C::OFF_T + s * C::TILE;
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks)
-            mma_ss(tmem + C::TM_S0 + b * 128, sdesc_kmajor<C::SWB, 128>(sb + C::OFF_Q, ks),
-                   sdesc_kmajor<C::SWB, 128>(kb, ks), idS, ks > 0);
+            mma_ts(tmem + C::TM_S0 + b * 128, tmem + C::TM_Q + ks * 8, sdesc_kmajor<C::SWB, 128>(kb, ks), idS, ks > 0);
           mma_commit(bar(C::B_SFULL + b));
           mma_commit(bar(C::B_EMPTY + s));
+          if (++b == C::NSB) b = 0, bpar ^= 1;
+          if ((s += 2) >= C::NSLOT) s -= C::NSLOT, spar ^= 1;
         }
         if (!ok) break;
-        mma_commit(bar(C::B_QFREE));
         w.next(c, hms);
       }
       mma_commit(bar(C::B_SDONE));  // drain point for teardown
     } else if (warp == 2 && lane == 0 && !skip) {
-      // ---------------------------------------------------------------- UMMA issuer: P V
-      constexpr uint32_t idO = idesc_bf16(128, D, false, true);
+      // ---------------------------------------------------------------- UMMA issuer: O += P V
+      constexpr uint32_t idO = FP8 ? idesc_f16(128, D, false, true) : idesc_bf16(128, D, false, true);
       bool ok = true;
-      int gs = 0, seg = 0;
+      int seg = 0, b = 0, s = 1;
+      uint32_t bpar = 0, spar = 0;
       for (; ok && w.more(); ++seg) {
         const int n = w.n();
-        for (int j = 0; j < n; ++j, ++gs) {
-          const int b = gs % C::NSB, it = 2 * gs + 1, s = it % C::NSLOT;
-          if (!(ok = mbar_wait(bar(C::B_PFULL + b), (gs / C::NSB) & 1, guard, SITE_TREE_MMA))) break;
-          if (!(ok = mbar_wait(bar(C::B_FULL + s), (it / C::NSLOT) & 1, guard, SITE_TREE_MMA))) break;
+        for (int j = 0; j < n; ++j) {
+          if (!(ok = mbar_wait(bar(C::B_PFULL + b), bpar, guard, SITE_TREE_MMA))) break;
+          if (!(ok = mbar_wait(bar(C::B_FULL + s), spar, guard, SITE_TREE_MMA))) break;
           // a unit's first product overwrites O: the epilogue before it has read it
           if (j == 0 && seg > 0 && !(ok = mbar_wait(bar(C::B_OFREE), (seg - 1) & 1, guard, SITE_TREE_MMA))) break;
           tc_fence_after();
@@ -399,6 +499,8 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::NTHREADS, 1)
             mma_ts(tmem + C::TM_O, aP + ks * 8, sdesc_mnmajor<C::SWB, 128>(vb, ks), idO, (j > 0 || ks > 0));
           mma_commit(bar(C::B_EMPTY + s));
           mma_commit(bar(C::B_PFREE + b));
+          if (++b == C::NSB) b = 0, bpar ^= 1;
+          if ((s += 2) >= C::NSLOT) s -= C::NSLOT, spar ^= 1;
         }
         if (!ok) break;
         mma_commit(bar(C::B_OFULL));
@@ -415,29 +517,86 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::NTHREADS, 1)
       const uint32_t tl = tmem + (static_cast<uint32_t>(wq * 32) << 16);
       const int tid = threadIdx.x - 128;
       float* rows = reinterpret_cast<float*>(smem + C::OFF_ROWS);
-      float4* xch = reinterpret_cast<float4*>(smem + C::OFF_M);
+      float4* xch = reinterpret_cast<float4*>(smem + C::OFF_Q + 32768 - 16384);
       const int boxes = c.page < kKeys ? kKeys / c.page : 1;
+      const uint32_t all_boxes = boxes == 1 ? 1u : (1u << boxes) - 1u;
       bool ok = true;
-      int gs = 0, seg = 0;
-      uint32_t meet_parity = 0;
-      // the four softmax warps meet; a wait with a limit like every other
+      int seg = 0, b = 0, vs_slot = 1, sc = 0;  // S buffer, slot of V, scales
+      uint32_t bpar = 0, vpar = 0, meet_parity = 0;
+      // The four softmax warps meet; a wait with a limit.  It does not look at the abort flag, so that
+      // either all four pass or none does, and what follows may use plain barriers.
       auto meet = [&]() -> bool {
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(C::B_MEET));
-        const bool all = mbar_wait_warp(bar(C::B_MEET), meet_parity, guard, SITE_TREE_SOFTMAX);
+        const uint64_t t0 = gtimer_ns();
+        bool all;
+        while (!(all = mbar_try(bar(C::B_MEET), meet_parity)) && gtimer_ns() - t0 <= 2 * kWaitLimitNs) {
+        }
         meet_parity ^= 1;
-        return all;
+        return __all_sync(0xffffffffu, all);
       };
+      // This thread's row of the next unit's Q into tensor memory; returns what a score is multiplied by.
+      // For an e4m3 cache the row becomes f16, scaled by a power of two to a maximum in [2^14, 2^15): elements
+      // of 2^-31 of the maximum and more keep all their bits.
+      float q_scale = 0.f;
+      auto take_q = [&](int s) -> bool {
+        if (!mbar_wait_warp(bar(C::B_Q), s & 1, guard, SITE_TREE_SOFTMAX)) return false;
+        const uint32_t qrow = sb + C::OFF_Q + r_in * C::SWB;
+        auto unit = [&](int u) {  // 8 elements
+          return ld_shared_v4(qrow + (u / (C::CE / 8)) * (GR * C::SWB) + (((u % (C::CE / 8)) ^ swz_row<C::SWB>(r_in)) << 4));
+        };
+        float mul = 1.f;
+        q_scale = p.c_log2;
+        if constexpr (FP8) {
+          uint32_t m = 0;
+#pragma unroll
+          for (int u = 0; u < D / 8; ++u) {
+            const uint4 v = unit(u);
+            const uint32_t k = 0x7fff7fffu;
+            m = __vmaxu2(m, __vmaxu2(__vmaxu2(v.x & k, v.y & k), __vmaxu2(v.z & k, v.w & k)));
+          }
+          int e = static_cast<int>(max(m & 0xffffu, m >> 16) >> 7);  // biased exponent of the largest
+          e = e < 15 ? 15 : e;
+          mul = __int_as_float((268 - e) << 23);                     // 2^(14 - (e - 127))
+          q_scale = p.c_log2 * __int_as_float((e - 14) << 23);
+        }
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k) {
+          uint32_t o[16];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint4 v = unit(4 * k + i);
+            const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              o[4 * i + e] = FP8 ? pack_f16x2(__uint_as_float(x[e] << 16) * mul,
+                                              __uint_as_float(x[e] & 0xffff0000u) * mul)
+                                 : x[e];
+          }
+          tmem_st16(tl + C::TM_Q + 16 * k, o);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar(C::B_QFREE));
+          mbar_arrive(bar(C::B_QREADY));
+        }
+        return true;
+      };
+      ok = take_q(0);
       for (; ok && w.more(); ++seg) {
         const int n = w.n();
         const int h = w.hm / p.M, mt = w.hm - h * p.M;
         const int q = mt * 128 + r_in, t = q % c.T;
         const int len = seq_len(c, w.b), nn = seq_new(c, w.b), prefix = seq_prefix(c, w.b);
+        const int inside = min(prefix, len);  // keys below it are seen by every live row
         const bool live = q < p.R && t < nn;  // rows that are not there see nothing
         const bool warp_live = mt * 128 + (wq * 32) % GR < p.R;
         const unsigned long long* trow =
             p.tree == nullptr ? nullptr : p.tree + w.b * p.tree_stride + static_cast<size_t>(t) * p.words;
-        SoftmaxRow st;
+        const float rq = q_scale;
+        float ref = -INFINITY, l = 0.f, lr = 0.f;  // reference, sum of weights, sum of weights as rounded
         Poison<D> poison;
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) poison.pos[i] = poison.neg[i] = 0u;
@@ -446,121 +605,51 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::NTHREADS, 1)
           return lane < boxes && j < len && page_of(c, w.b, j) >= 0;
         };
         bool there = pages_there(w.t0);
-        for (int j = 0; j < n; ++j, ++gs) {
-          const int b = gs % C::NSB, k0 = (w.t0 + j) * kKeys;
+        for (int j = 0; j < n; ++j) {
+          const int k0 = (w.t0 + j) * kKeys;
           const uint32_t pm = __ballot_sync(0xffffffffu, there);
           if (j + 1 < n) there = pages_there(w.t0 + j + 1);
-          const int inside = min(prefix, len);  // keys below it are seen by every live row
-          const bool edge = k0 + kKeys > inside || pm != (boxes == 1 ? 1u : (1u << boxes) - 1u);
-          if (!(ok = mbar_wait_warp(bar(C::B_SFULL + b), (gs / C::NSB) & 1, guard, SITE_TREE_SOFTMAX))) break;
+          const bool edge = k0 + kKeys > inside || pm != all_boxes;
+          if (!(ok = mbar_wait_warp(bar(C::B_SFULL + b), bpar, guard, SITE_TREE_SOFTMAX))) break;
           tc_fence_after();
           uint32_t seen[GR / 32];  // this row's keys of its group, 32 a word
           if (edge) {
 #pragma unroll
             for (int i = 0; i < GR / 32; ++i) {
-              const int j0 = k0 + group * GR + 32 * i;
+              const int off = group * GR + 32 * i, j0 = k0 + off;
               uint32_t m = low_bits(inside - j0);
               if (j0 + 32 > prefix) m |= draft_bits(trow, p.words, t, j0 - prefix);
               m &= low_bits(len - j0);
-              if (boxes == 8) {  // pages of 16
-                const int bx = (group * GR + 32 * i) / 16;
-                m &= ((pm >> bx) & 1u ? 0xffffu : 0u) | ((pm >> (bx + 1)) & 1u ? 0xffff0000u : 0u);
-              } else if (!((pm >> ((group * GR + 32 * i) * boxes / kKeys)) & 1u)) {
-                m = 0u;
-              }
-              seen[i] = live ? m : 0u;
+              const int bx = off * boxes / kKeys;
+              uint32_t in_page = (pm >> bx) & 1u ? 0xffffffffu : 0u;
+              if (boxes == 8) in_page = (in_page & 0xffffu) | ((pm >> (bx + 1)) & 1u ? 0xffff0000u : 0u);  // pages of 16
+              seen[i] = live ? m & in_page : 0u;
             }
-          }
-          if (k0 + kKeys > inside) {
-            // the tile holds drafted tokens or rows behind the end
-            const int it = 2 * gs + 1, s = it % C::NSLOT;
-            if (!(ok = mbar_wait_warp(bar(C::B_FULL + s), (it / C::NSLOT) & 1, guard, SITE_TREE_SOFTMAX))) break;
-            const uint32_t vb = sb + C::OFF_T + s * C::TILE;
-            const int key = k0 + row;  // this thread looks after one value row
-            uint32_t vpos[D / 32], vneg[D / 32];
-            bool bad = false;
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i) vpos[i] = vneg[i] = 0u;
-            if (key >= inside) {
-              // a single token sees itself (or nothing at all): its values need no look
-              const bool look = key < len && !(c.T == 1 && p.tree == nullptr);
-#pragma unroll
-              for (int u = 0; u < D / 8; ++u) {
-                const uint32_t at = vb + (u * 8 / C::CE) * (128 * C::SWB) + row * C::SWB +
-                                    (((u * 8 % C::CE / 8) ^ swz_row<C::SWB>(row)) << 4);
-                if (key >= len) {
-                  asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0u) : "memory");
-                } else if (look) {
-                  uint32_t x[4];
-                  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                               : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
-                               : "r"(at)
-                               : "memory");
-                  bool here = false;
-#pragma unroll
-                  for (int e = 0; e < 8; ++e) {
-                    const uint32_t half = x[e / 2] >> (16 * (e & 1)) & 0xffffu;
-                    if ((half & 0x7f80u) == 0x7f80u) {
-                      here = true;
-                      const bool nan = (half & 0x7fu) != 0;
-                      const uint32_t bit = 1u << ((u * 8 + e) & 31);
-                      if (nan || !(half >> 15)) vpos[u / 4] |= bit;
-                      if (nan || half >> 15) vneg[u / 4] |= bit;
-                      x[e / 2] &= ~(0xffffu << (16 * (e & 1)));
-                    }
-                  }
-                  if (here) {
-                    bad = true;
-                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x[0]), "r"(x[1]), "r"(x[2]),
-                                 "r"(x[3])
-                                 : "memory");
-                  }
-                }
-              }
-              fence_proxy_async_smem();  // the product reads what was written here
+            if (k0 + kKeys > inside) {  // the tile holds drafted tokens or rows behind the end
+              if (!(ok = mbar_wait_warp(bar(C::B_FULL + vs_slot), vpar, guard, SITE_TREE_SOFTMAX)) || !(ok = meet()))
+                break;
+              clean_values<D, FP8, GR>(sb + C::OFF_T + vs_slot * C::TILE, row, k0 + row, inside, len,
+                                       c.T > 1 || p.tree != nullptr, group, seen, poison, bad_rows, bad_stage);
             }
-            const uint32_t badw = __ballot_sync(0xffffffffu, bad);
-            if (lane == 0) bad_rows[wq] = badw;
-            if (!(ok = meet())) break;
-            uint32_t bw[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) bw[i] = bad_rows[i];
-            if ((bw[0] | bw[1] | bw[2] | bw[3]) != 0) {  // hand each such row to the rows that see it
-#pragma unroll 1
-              for (int i = 0; ok && i < 128; ++i) {
-                if (!((bw[i >> 5] >> (i & 31)) & 1u)) continue;
-                if (row == i) {
-#pragma unroll
-                  for (int e = 0; e < D / 32; ++e) {
-                    bad_stage[e] = vpos[e];
-                    bad_stage[4 + e] = vneg[e];
-                  }
-                }
-                if (!(ok = meet())) break;
-                const int k = i - group * GR;
-                bool sees = false;
-#pragma unroll
-                for (int e = 0; e < GR / 32; ++e)
-                  if (k >= 32 * e && k < 32 * e + 32) sees = seen[e] >> (k & 31) & 1u;
-                if (sees) {
-#pragma unroll
-                  for (int e = 0; e < D / 32; ++e) {
-                    poison.pos[e] |= bad_stage[e];
-                    poison.neg[e] |= bad_stage[4 + e];
-                  }
-                }
-                ok = meet();
-              }
-            }
-            if (!ok || !(ok = meet())) break;  // bad_rows may be written again
           }
           if (warp_live) {
+            uint32_t r[GR];
             float s[GR];
-            {
-              uint32_t r[GR];
 #pragma unroll
-              for (int i = 0; i < GR / 32; ++i) tmem_ld32(tl + C::TM_S0 + b * 128 + group * GR + 32 * i, r + 32 * i);
-              tmem_ld_wait<GR>(r);
+            for (int i = 0; i < GR / 32; ++i) tmem_ld32(tl + C::TM_S0 + b * 128 + group * GR + 32 * i, r + 32 * i);
+            tmem_ld_wait<GR>(r);
+            // scores in base-2 units, and for each row the largest of what decides the weights' range
+            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            const uint32_t scales = sb + C::OFF_SCALE + sc * 1536 + group * GR * 4;
+            if constexpr (FP8) {
+#pragma unroll
+              for (int k = 0; k < GR; k += 4) {
+                const uint4 ks = ld_shared_v4(scales + 4 * k);
+                const uint32_t kk[4] = {ks.x, ks.y, ks.z, ks.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[k + e] = __uint_as_float(r[k + e]) * rq * __uint_as_float(kk[e]);
+              }
+            } else {
 #pragma unroll
               for (int k = 0; k < GR; ++k) s[k] = __uint_as_float(r[k]);
             }
@@ -569,33 +658,36 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::NTHREADS, 1)
               for (int k = 0; k < GR; ++k)
                 if (!((seen[k / 32] >> (k & 31)) & 1u)) s[k] = -INFINITY;
             }
-            float m4[4];
 #pragma unroll
-            for (int a = 0; a < 4; ++a) {
-              constexpr int Q4 = GR / 4;
-              m4[a] = fmaxf(s[a * Q4], s[a * Q4 + 1]);
+            for (int k = 0; k < GR; k += 8) {
+              float v[8];
 #pragma unroll
-              for (int k = 2; k < Q4; k += 2) m4[a] = fmax3(m4[a], s[a * Q4 + k], s[a * Q4 + k + 1]);
+              for (int e = 0; e < 8; ++e) v[e] = s[k + e];
+              if constexpr (FP8) {
+                const uint4 a = ld_shared_v4(scales + 1024 + 4 * k), bb = ld_shared_v4(scales + 1024 + 4 * k + 16);
+                v[0] += __uint_as_float(a.x), v[1] += __uint_as_float(a.y), v[2] += __uint_as_float(a.z);
+                v[3] += __uint_as_float(a.w), v[4] += __uint_as_float(bb.x), v[5] += __uint_as_float(bb.y);
+                v[6] += __uint_as_float(bb.z), v[7] += __uint_as_float(bb.w);
+              }
+#pragma unroll
+              for (int e = 0; e < 4; ++e) top[e] = fmax3(top[e], v[2 * e], v[2 * e + 1]);
             }
-            const float m_tile = fmaxf(fmax3(m4[0], m4[1], m4[2]), m4[3]) * p.c_log2;
+            float tile_top = fmaxf(fmax3(top[0], top[1], top[2]), top[3]);
+            if constexpr (!FP8) tile_top *= p.c_log2;
+            constexpr float kStart = FP8 ? -kF16Start : kFwdMaxHeadroom, kMove = FP8 ? kF16Top : kFwdRescaleThreshold;
             if (j == 0) {
-              st.m_run = m_tile + kFwdMaxHeadroom;
+              ref = tile_top + kStart;
             } else {
-              const bool move = m_tile > st.m_run + kFwdRescaleThreshold;
+              const bool move = tile_top > ref + kMove;
               if (__any_sync(0xffffffffu, move)) {
-                const float m_new = m_tile + kFwdMaxHeadroom;
-                const float alpha = move ? ex2(st.m_run - m_new) : 1.f;
-                if (move) {
-                  st.l_run *= alpha;
-                  st.lr_run *= alpha;
-                  st.m_run = m_new;
-                }
-                // the product that last wrote O is done
-                if (!(ok = mbar_wait_warp(bar(C::B_PFREE + (gs - 1) % C::NSB), ((gs - 1) / C::NSB) & 1, guard,
-                                          SITE_TREE_SOFTMAX)))
-                  break;
+                const float new_ref = tile_top + kStart;
+                const float alpha = move ? ex2(ref - new_ref) : 1.f;
+                if (move) l *= alpha, lr *= alpha, ref = new_ref;
+                // the product that last wrote O is done: it read the S buffer before this one
+                const int pb = b == 0 ? C::NSB - 1 : b - 1;
+                if (!(ok = mbar_wait_warp(bar(C::B_PFREE + pb), b == 0 ? bpar ^ 1 : bpar, guard, SITE_TREE_SOFTMAX))) break;
                 tc_fence_after();
-#pragma unroll
+#pragma unroll 1
                 for (int i = 0; i < D / 32; ++i) {
                   uint32_t o[32];
                   tmem_ld32(tl + C::TM_O + 32 * i, o);
@@ -607,25 +699,42 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::NTHREADS, 1)
                 tmem_st_wait();
               }
             }
-            const float neg_m = st.m_run == -INFINITY ? 0.f : -st.m_run;  // nothing seen so far: P = 0
-            const uint64_t cc2 = f2pack(p.c_log2, p.c_log2), nm2 = f2pack(neg_m, neg_m);
+            const float neg = ref == -INFINITY ? 0.f : -ref;  // nothing seen so far: every weight is 0
+            const uint64_t neg2 = f2pack(neg, neg), cc2 = f2pack(p.c_log2, p.c_log2);
             uint64_t ls[2] = {f2pack(0.f, 0.f), f2pack(0.f, 0.f)};
             float rl[2] = {0.f, 0.f}, rh[2] = {0.f, 0.f};
             uint32_t pk[GR / 2];
 #pragma unroll
-            for (int k = 0; k < GR; k += 2) {
-              float t0, t1;
-              f2unpack(ffma2(f2pack(s[k], s[k + 1]), cc2, nm2), t0, t1);
-              const float p0 = ex2(t0), p1 = ex2(t1);
-              ls[(k >> 1) & 1] = fadd2(ls[(k >> 1) & 1], f2pack(p0, p1));
-              const uint32_t v = pack_bf16x2(p0, p1);
-              pk[k >> 1] = v;
-              add_bf16x2_f32(v, rl[(k >> 1) & 1], rh[(k >> 1) & 1]);
+            for (int k = 0; k < GR; k += 4) {
+              uint64_t vsc[2];
+              if constexpr (FP8) {
+                const uint4 a = ld_shared_v4(scales + 512 + 4 * k);
+                vsc[0] = f2pack(__uint_as_float(a.x), __uint_as_float(a.y));
+                vsc[1] = f2pack(__uint_as_float(a.z), __uint_as_float(a.w));
+              }
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const uint64_t x = f2pack(s[k + 2 * e], s[k + 2 * e + 1]);
+                float t0, t1;
+                f2unpack(FP8 ? fadd2(x, neg2) : ffma2(x, cc2, neg2), t0, t1);
+                const uint64_t w2 = f2pack(ex2(t0), ex2(t1));
+                ls[e] = fadd2(ls[e], w2);
+                float p0, p1;
+                if constexpr (FP8) {
+                  f2unpack(fmul2(w2, vsc[e]), p0, p1);
+                  pk[k / 2 + e] = pack_f16x2(p0, p1);
+                } else {
+                  f2unpack(w2, p0, p1);
+                  pk[k / 2 + e] = pack_bf16x2(p0, p1);
+                  add_bf16x2_f32(pk[k / 2 + e], rl[e], rh[e]);
+                }
+              }
             }
             float a0, a1;
             f2unpack(fadd2(ls[0], ls[1]), a0, a1);
-            st.l_run += a0 + a1;
-            st.lr_run += (rl[0] + rl[1]) + (rh[0] + rh[1]);
+            l += a0 + a1;
+            // bf16 weights are normalised by their own sum; f16 ones are off by 2^-11 at most
+            lr = FP8 ? l : lr + (rl[0] + rl[1]) + (rh[0] + rh[1]);
             // own keys' weights, zeros for the other groups'
             if constexpr (NS == 1) {
               tmem_st32(tl + C::TM_S0 + b * 128, pk);
@@ -637,8 +746,13 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::NTHREADS, 1)
 #pragma unroll
               for (int g = 0; g < NS; ++g) {
                 const uint32_t at = tl + C::TM_S0 + b * 128 + g * (GR / 2);
-                if constexpr (NS == 2) tmem_st32(at, g == group ? pk : zero);
-                else tmem_st16(at, g == group ? pk : zero);
+                if (g == group) {
+                  if constexpr (NS == 2) tmem_st32(at, pk);
+                  else tmem_st16(at, pk);
+                } else {
+                  if constexpr (NS == 2) tmem_st32(at, zero);
+                  else tmem_st16(at, zero);
+                }
               }
             }
             tmem_st_wait();
@@ -646,85 +760,104 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::NTHREADS, 1)
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(C::B_PFULL + b));
+          if (++b == C::NSB) b = 0, bpar ^= 1;
+          if ((vs_slot += 2) >= C::NSLOT) vs_slot -= C::NSLOT, vpar ^= 1;
+          if (FP8 && ++sc == C::NSC) sc = 0;
         }
         if (!ok) break;
         // ------------------------------------------------------------ this run's part of the unit is done
-        if (!(ok = mbar_wait_warp(bar(C::B_OFULL), seg & 1, guard, SITE_TREE_SOFTMAX))) break;
+        const Walk at = w;
+        w.next(c, hms);
+        if (w.more() && !(ok = take_q(seg + 1))) break;  // the next unit's S may be formed meanwhile
+        if (!(ok = mbar_wait_warp(bar(C::B_OFULL), seg & 1, guard, SITE_TREE_SOFTMAX)) || !(ok = meet())) break;
         tc_fence_after();
-        const bool whole = w.t0 == 0 && n == w.nt;
-        const long long unit = static_cast<long long>(w.b) * hms + w.hm;
-        if (w.t0 == 0 && tid == 0) {
-          const long long at = lo + mine - w.left;  // the unit's first tile among all tiles
-          p.info[unit] = UnitInfo{static_cast<int>(blockIdx.x), static_cast<int>((at + w.nt - 1) / run)};
+        const bool whole = at.t0 == 0 && n == at.nt;
+        if (at.t0 == 0 && tid == 0) {
+          const long long first = lo + mine - at.left;  // the unit's first tile among all tiles
+          p.info[static_cast<long long>(at.b) * hms + at.hm] =
+              UnitInfo{static_cast<int>(blockIdx.x), static_cast<int>((first + at.nt - 1) / run)};
         }
         // a NaN score does not move the maximum: where nothing else is seen it is still -inf
-        if (st.lr_run != st.lr_run) st.m_run = st.lr_run;
-        if (!live) st = SoftmaxRow();  // whatever its lane computed
-        rows[row] = st.m_run;
-        rows[128 + row] = st.l_run;
-        rows[256 + row] = st.lr_run;
-        if (!(ok = meet())) break;
-        // the groups' common reference and sums
-        float mx = -INFINITY;
+        if (lr != lr) ref = lr;
+        if (!live) ref = -INFINITY, l = lr = 0.f;  // whatever its lane computed
+        float f = 1.f;  // this group's share in the row's common reference
+        float om = ref, ol = l, olr = lr;
+        const int orow = tid / NS, opart = tid % NS;  // the row this thread stores its share of
+        if constexpr (NS > 1) {
+          rows[row] = ref;
+          rows[128 + row] = l;
+          rows[256 + row] = lr;
+          named_bar_sync(1, 128);
+          float mx = -INFINITY;
+          om = -INFINITY, ol = olr = 0.f;
 #pragma unroll
-        for (int g = 0; g < NS; ++g) mx = fmaxf(mx, rows[g * GR + r_in]);
-        const float f = st.m_run == -INFINITY ? 0.f : ex2(st.m_run - mx);
-        // the row this thread stores its share of
-        constexpr int TPR = NS, CPT = 8 / NS;  // threads per stored row; 16-byte pieces of 32 columns each
-        const int orow = tid / TPR, opart = tid % TPR;
-        float om = -INFINITY, ol = 0.f, olr = 0.f;
+          for (int g = 0; g < NS; ++g) {
+            mx = fmaxf(mx, rows[g * GR + r_in]);
+            om = fmaxf(om, rows[g * GR + orow]);
+          }
+          f = ref == -INFINITY ? 0.f : ex2(ref - mx);
 #pragma unroll
-        for (int g = 0; g < NS; ++g) om = fmaxf(om, rows[g * GR + orow]);
-#pragma unroll
-        for (int g = 0; g < NS; ++g) {
-          const float mg = rows[g * GR + orow];
-          const float fg = mg == -INFINITY ? 0.f : ex2(mg - om);
-          ol += fg * rows[128 + g * GR + orow];
-          olr += fg * rows[256 + g * GR + orow];
+          for (int g = 0; g < NS; ++g) {
+            const float mg = rows[g * GR + orow];
+            const float fg = mg == -INFINITY ? 0.f : ex2(mg - om);
+            ol += fg * rows[128 + g * GR + orow];
+            olr += fg * rows[256 + g * GR + orow];
+          }
+          if (olr != olr) om = olr;  // so that the join keeps the row
         }
-        if (olr != olr) om = olr;  // so that the join keeps the row
         const int oq = mt * 128 + orow;
         const bool store = oq < p.R;
-        const size_t grow = (static_cast<size_t>(w.b) * c.Hk + h) * p.R + oq;
-        float* slot = p.part + (2 * static_cast<size_t>(blockIdx.x) + (w.t0 == 0 ? 1 : 0)) * p.rows * (D + 3);
+        const size_t grow = (static_cast<size_t>(at.b) * c.Hk + h) * p.R + oq;
+        float* slot = p.part + (2 * static_cast<size_t>(blockIdx.x) + (at.t0 == 0 ? 1 : 0)) * p.rows * (D + 3);
         const float inv = olr == 0.f ? 0.f : 1.f / olr;
-#pragma unroll
+        // 32 columns at a time (a loop, not unrolled: this code runs once per unit, and fetching it costs more
+        // than the jumps)
+#pragma unroll 1
         for (int i = 0; i < D / 32; ++i) {
-          if (!ok) continue;
           uint32_t o[32];
           tmem_ld32(tl + C::TM_O + 32 * i, o);
           tmem_ld_wait<32>(o);
-          if (poison.pos[i] | poison.neg[i]) {
+          uint32_t pp = 0, pn = 0;
+#pragma unroll
+          for (int e = 0; e < D / 32; ++e)
+            if (e == i) pp = poison.pos[e], pn = poison.neg[e];
+          if (pp | pn) {
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
-              const bool a = poison.pos[i] >> e & 1u, d = poison.neg[i] >> e & 1u;
+              const bool a = pp >> e & 1u, d = pn >> e & 1u;
               if (a || d)
                 o[e] = __float_as_uint(__uint_as_float(o[e]) +
                                        (a && d ? __int_as_float(0x7fffffff) : a ? INFINITY : -INFINITY));
             }
           }
-          if (i > 0 && !(ok = meet())) continue;  // the piece before has been read
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            float4 v;
-            v.x = f == 0.f ? 0.f : __uint_as_float(o[4 * k]) * f;
-            v.y = f == 0.f ? 0.f : __uint_as_float(o[4 * k + 1]) * f;
-            v.z = f == 0.f ? 0.f : __uint_as_float(o[4 * k + 2]) * f;
-            v.w = f == 0.f ? 0.f : __uint_as_float(o[4 * k + 3]) * f;
-            xch[row * 8 + (k ^ (row & 7))] = v;
-          }
-          if (!(ok = meet())) continue;
+          constexpr int CPT = 8 / NS;  // 16-byte pieces of the 32 columns that a thread stores
           float a[4 * CPT];
+          if constexpr (NS == 1) {
 #pragma unroll
-          for (int k = 0; k < CPT; ++k) {
-            const int piece = opart * CPT + k;
-            float4 v = xch[orow * 8 + (piece ^ (orow & 7))];
+            for (int k = 0; k < 32; ++k) a[k] = lr == 0.f ? 0.f : __uint_as_float(o[k]);
+          } else {
+            if (i > 0) named_bar_sync(1, 128);  // the columns before have been read
 #pragma unroll
-            for (int g = 1; g < NS; ++g) {
-              const float4 y = xch[(g * GR + orow) * 8 + (piece ^ ((g * GR + orow) & 7))];
-              v.x += y.x, v.y += y.y, v.z += y.z, v.w += y.w;
+            for (int k = 0; k < 8; ++k) {
+              float4 v;
+              v.x = f == 0.f ? 0.f : __uint_as_float(o[4 * k]) * f;
+              v.y = f == 0.f ? 0.f : __uint_as_float(o[4 * k + 1]) * f;
+              v.z = f == 0.f ? 0.f : __uint_as_float(o[4 * k + 2]) * f;
+              v.w = f == 0.f ? 0.f : __uint_as_float(o[4 * k + 3]) * f;
+              xch[row * 8 + (k ^ (row & 7))] = v;
             }
-            a[4 * k] = v.x, a[4 * k + 1] = v.y, a[4 * k + 2] = v.z, a[4 * k + 3] = v.w;
+            named_bar_sync(1, 128);
+#pragma unroll
+            for (int k = 0; k < CPT; ++k) {
+              const int piece = opart * CPT + k;
+              float4 v = xch[orow * 8 + (piece ^ (orow & 7))];
+#pragma unroll
+              for (int g = 1; g < NS; ++g) {
+                const float4 y = xch[(g * GR + orow) * 8 + (piece ^ ((g * GR + orow) & 7))];
+                v.x += y.x, v.y += y.y, v.z += y.z, v.w += y.w;
+              }
+              a[4 * k] = v.x, a[4 * k + 1] = v.y, a[4 * k + 2] = v.z, a[4 * k + 3] = v.w;
+            }
           }
           if (store) {
             const int col = 32 * i + opart * CPT * 4;
@@ -743,7 +876,6 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::NTHREADS, 1)
             }
           }
         }
-        if (!ok) break;
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(C::B_OFREE));
@@ -757,60 +889,57 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::NTHREADS, 1)
             ml[2 * p.rows + orow] = olr;
           }
         }
-        if (!(ok = meet())) break;  // rows and the exchange are free again
-        w.next(c, hms);
+        if constexpr (NS > 1) named_bar_sync(1, 128);  // rows and the exchange are free again
       }
     }
   } else if constexpr (FP8) {
     regs_dec<112>();
     if (!skip) {
-      // ---------------------------------------------------------------- e4m3 -> bf16 tiles
-      const int tid = threadIdx.x - 256;
-      constexpr int PPR = D / 16;  // 16-byte pieces of an e4m3 row
+      // ---------------------------------------------------------------- e4m3 -> f16 tiles
+      // Warps 8..11 take the K tiles, 12..15 the V tiles: two tiles under way at once.
+      const int kv = (warp - 8) >> 2, tid = (threadIdx.x - 256) & 127;
+      constexpr int PPR = D / 16, NP = PPR;  // 16-byte pieces of an e4m3 row; of a thread
       bool ok = true;
-      int rs = 0, s = 0;                      // slots of the two rings
-      uint32_t rparity = 0, parity = 1;
-      // (a fresh barrier's phase of parity 1 counts as complete: the first trips do not wait)
-      for (long long left = 2 * mine; ok && left > 0; --left) {
-        if (!(ok = mbar_wait_warp(bar(C::B_RFULL + rs), rparity, guard, SITE_TREE_CONVERT))) break;
-        if (!(ok = mbar_wait_warp(bar(C::B_EMPTY + s), parity, guard, SITE_TREE_CONVERT))) break;
-        const uint8_t* raw = smem + C::OFF_RAW + rs * C::RAW;
-        const uint32_t dst = sb + C::OFF_T + s * C::TILE;
+      int rs = kv % C::NRAW, s = kv, sc = 0;  // slots of the rings
+      uint32_t rpar = 0, spar = 1;
+      for (long long left = mine; ok && left > 0; --left) {
+        if (!(ok = mbar_wait_warp(bar(C::B_RFULL + rs), rpar, guard, SITE_TREE_CONVERT))) break;
+        const uint32_t raw = sb + C::OFF_RAW + rs * C::RAW, dst = sb + C::OFF_T + s * C::TILE;
+        uint4 x[NP];
 #pragma unroll
-        for (int k = 0; k < 128 * PPR / 256; ++k) {
-          const int piece = k * 256 + tid, row = piece / PPR, sub = piece % PPR;
-          const uint4 x = *reinterpret_cast<const uint4*>(raw + piece * 16);
-          const int e = raw[128 * D + row];
-          const int e1 = e < 134 ? e : 134;
-          uint32_t m1 = static_cast<uint32_t>(e1 + 120) << 7;
-          m1 |= m1 << 16;
-          const uint32_t w4[4] = {x.x, x.y, x.z, x.w};
+        for (int k = 0; k < NP; ++k) x[k] = ld_shared_v4(raw + (k * 128 + tid) * 16);
+        if (!(ok = mbar_wait_warp(bar(C::B_EMPTY + s), spar, guard, SITE_TREE_CONVERT))) break;
+        if (kv == 0) {
+          // The tile's scales, for the softmax warps.  This slot held the K tile NSLOT / 2 tiles ago, whose S is
+          // done; so the P of NSB tiles before that was used, and the softmax is past it: the NSLOT / 2 + NSB - 1
+          // tiles it may still read are not overwritten.
+          const uint8_t* exps = smem + C::OFF_RAW + rs * C::RAW + 128 * D;
+          float* scale = reinterpret_cast<float*>(smem + C::OFF_SCALE) + sc * 384 + tid;
+          const int ek = exps[tid], ev = exps[128 + tid];
+          // (a row that holds NaN has NaN elements: its scale is 1)
+          scale[0] = ek == kExpNaN ? 1.f : __int_as_float(ek << 23);
+          scale[128] = ev == kExpNaN ? 1.f : __int_as_float(ev << 23);
+          scale[256] = ev == kExpNaN ? 0.f : static_cast<float>(ev - 127);
+          if (++sc == C::NSC) sc = 0;
+        }
+#pragma unroll
+        for (int k = 0; k < NP; ++k) {
+          const int piece = k * 128 + tid, row = piece / PPR, sub = piece % PPR;
+          const uint32_t w4[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
           uint32_t o[8];
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            o[2 * q] = bf16_mul2(spread_e4m3(__byte_perm(w4[q], 0, 0x1404)), m1);
-            o[2 * q + 1] = bf16_mul2(spread_e4m3(__byte_perm(w4[q], 0, 0x3424)), m1);
-          }
-          if (e > 134) {  // rare: rows with magnitudes above 57344, or that hold NaN
-            uint32_t m2 = e == kExpNaN ? 0x7fffu : static_cast<uint32_t>(127 + e - 134) << 7;
-            m2 |= m2 << 16;
-#pragma unroll
-            for (int q = 0; q < 8; ++q) o[q] = bf16_mul2(o[q], m2);
+            o[2 * q] = e4m3x2_to_f16x2(w4[q] & 0xffffu);
+            o[2 * q + 1] = e4m3x2_to_f16x2(w4[q] >> 16);
           }
           // the row's 16-byte units 2 sub and 2 sub + 1; lanes of the upper half of a wide row
           // write them in the other order, so that 8 lanes always hit 8 different units
-          const int flip = (sub * 2 / (C::CE / 8)) & 1;
+          const bool flip = (sub * 2 / (C::CE / 8)) & 1;
           const uint32_t base = dst + (sub * 16 / C::CE) * (128 * C::SWB) + row * C::SWB;
-          const int u0 = sub * 16 % C::CE / 8;
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            const int half = q ^ flip;
-            const uint32_t at = base + ((static_cast<uint32_t>(u0 + half) ^ swz_row<C::SWB>(row)) << 4);
-            const uint32_t v0 = half ? o[4] : o[0], v1 = half ? o[5] : o[1], v2 = half ? o[6] : o[2],
-                           v3 = half ? o[7] : o[3];
-            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v0), "r"(v1), "r"(v2), "r"(v3)
-                         : "memory");
-          }
+          const uint32_t u0 = sub * 16 % C::CE / 8, sw = swz_row<C::SWB>(row);
+          const uint4 lo4 = make_uint4(o[0], o[1], o[2], o[3]), hi4 = make_uint4(o[4], o[5], o[6], o[7]);
+          st_shared_v4(base + (((u0 + (flip ? 1 : 0)) ^ sw) << 4), flip ? hi4 : lo4);
+          st_shared_v4(base + (((u0 + (flip ? 0 : 1)) ^ sw) << 4), flip ? lo4 : hi4);
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -818,8 +947,8 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::NTHREADS, 1)
           mbar_arrive(bar(C::B_FULL + s));
           mbar_arrive(bar(C::B_REMPTY + rs));
         }
-        if (++rs == C::NRAW) rs = 0, rparity ^= 1;
-        if (++s == C::NSLOT) s = 0, parity ^= 1;
+        if ((rs += 2) >= C::NRAW) rs -= C::NRAW, rpar ^= 1;
+        if ((s += 2) >= C::NSLOT) s -= C::NSLOT, spar ^= 1;
       }
     }
   }
