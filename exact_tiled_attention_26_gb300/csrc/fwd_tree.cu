@@ -74,20 +74,23 @@ struct TreeArgs {
   int* status;
 };
 
-template <int D, bool FP8>
+template <int D, bool FP8, int NS>
 struct TCfg {
   static constexpr int SWB = (D * 2 >= 128) ? 128 : D * 2;
   static constexpr int CE = SWB / 2;
   static constexpr int NCH = D / CE;
   static constexpr int TILE = 128 * D * 2;
   static constexpr int NSLOT = FP8 ? (D == 128 ? 4 : 6) : (D == 128 ? 6 : 8);  // 16-bit tiles, K and V in turn
-  static constexpr int NRAW = FP8 ? (D == 128 ? 3 : 6) : 0;                    // e4m3 tiles
+  // Q (128 / NS rows) and, for NS > 1, 16 KB of the epilogue's exchange
+  static constexpr int QX = (128 / NS) * D * 2 + (NS > 1 ? 16384 : 0);
+  static constexpr int NRAW = FP8 ? (D == 128 ? (NS == 4 ? 4 : 3) : 6) : 0;    // e4m3 tiles: what fits
   static constexpr int RAW = 128 * D + 256;     // with the exponent bytes of its keys (K tiles: and of their values)
   static constexpr int NSB = D == 128 ? 2 : 3;  // S / P buffers in tensor memory
   static constexpr int NSC = FP8 ? NSLOT / 2 + NSB : 0;  // tiles whose scales are kept (see the converter)
   static constexpr int OFF_T = 0;
-  static constexpr int OFF_Q = OFF_T + NSLOT * TILE;     // 128 / NS rows; the epilogue's exchange (NS > 1) behind them
-  static constexpr int OFF_RAW = OFF_Q + 32768;
+  static constexpr int OFF_Q = OFF_T + NSLOT * TILE;
+  static constexpr int OFF_X = OFF_Q + (128 / NS) * D * 2;
+  static constexpr int OFF_RAW = OFF_Q + QX;
   static constexpr int OFF_SCALE = OFF_RAW + NRAW * RAW;  // [NSC][3][128] floats: 2^k of K, 2^k of V, k of V
   static constexpr int OFF_ROWS = OFF_SCALE + NSC * 3 * 128 * 4;  // [3][128] floats
   static constexpr int OFF_BAR = OFF_ROWS + 3 * 128 * 4;
@@ -108,6 +111,13 @@ struct TCfg {
 FA_DEV int tiles_of(const CacheView& c, int b) {
   const int n = (seq_len(c, b) + kKeys - 1) / kKeys;
   return n < 1 ? 1 : n;  // an empty sequence passes through as one masked tile
+}
+
+// 64-bit quotients of what nearly always fits in 32 bits (a 64-bit division takes some
+// hundred instructions).
+FA_DEV long long quotient(long long a, long long b) {
+  if (((a | b) >> 31) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
 }
 
 // A CTA's run of tiles, unit by unit.
@@ -207,11 +217,12 @@ FA_DEV uint32_t swz_row(int row) {
 // reach every row of the product; infinities and NaNs of drafted tokens are taken out and
 // noted in the poison of the rows that see the token.  Loops stay loops: the code runs once
 // or twice per unit.
-template <int D, bool FP8, int GR>
+template <int D, bool FP8, int NS>
 FA_DEV void clean_values(uint32_t tile, int row, int key, int inside, int len, bool look, int group,
                          const uint32_t* seen, Poison<D>& poison, volatile uint32_t* bad_rows,
                          volatile uint32_t* bad_stage) {
-  using C = TCfg<D, FP8>;
+  using C = TCfg<D, FP8, NS>;
+  constexpr int GR = 128 / NS;
   constexpr uint32_t EXP = FP8 ? 0x7c00u : 0x7f80u, MANT = FP8 ? 0x03ffu : 0x007fu;
   const int lane = row & 31;
   auto unit = [&](int u) {
@@ -288,10 +299,10 @@ FA_DEV void clean_values(uint32_t tile, int row, int key, int inside, int len, b
 }
 
 template <int D, bool FP8, int NS>
-__global__ void __launch_bounds__(TCfg<D, FP8>::NTHREADS, 1)
+__global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
     tree_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                 const __grid_constant__ CUtensorMap tmV, const __grid_constant__ TreeArgs p) {
-  using C = TCfg<D, FP8>;
+  using C = TCfg<D, FP8, NS>;
   constexpr int GR = 128 / NS;  // rows of a group, and keys each group weighs
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
@@ -347,7 +358,7 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::NTHREADS, 1)
     for (int b = b0; b < b1; ++b) sum += tiles_of(c, b);
     const long long before = block_prefix<C::NTHREADS>(sum, scratch, &total);
     total *= hms;
-    run = (total + gridDim.x - 1) / gridDim.x;
+    run = quotient(total + gridDim.x - 1, gridDim.x);
     lo = run * blockIdx.x;
     mine = total - lo < run ? total - lo : run;
     if (mine > 0 && lo >= before * hms && lo < (before + sum) * hms) {
@@ -360,8 +371,9 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::NTHREADS, 1)
       }
       const int nt = tiles_of(c, b);
       start[0] = b;
-      start[1] = static_cast<int>((lo - at) / nt);
-      start[2] = static_cast<int>((lo - at) % nt);
+      const int hm = static_cast<int>(quotient(lo - at, nt));
+      start[1] = hm;
+      start[2] = static_cast<int>(lo - at - static_cast<long long>(hm) * nt);
     }
   }
   tc_fence_before();
@@ -517,7 +529,7 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::NTHREADS, 1)
       const uint32_t tl = tmem + (static_cast<uint32_t>(wq * 32) << 16);
       const int tid = threadIdx.x - 128;
       float* rows = reinterpret_cast<float*>(smem + C::OFF_ROWS);
-      float4* xch = reinterpret_cast<float4*>(smem + C::OFF_Q + 32768 - 16384);
+      float4* xch = reinterpret_cast<float4*>(smem + C::OFF_X);
       const int boxes = c.page < kKeys ? kKeys / c.page : 1;
       const uint32_t all_boxes = boxes == 1 ? 1u : (1u << boxes) - 1u;
       bool ok = true;
@@ -610,8 +622,6 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::NTHREADS, 1)
           const uint32_t pm = __ballot_sync(0xffffffffu, there);
           if (j + 1 < n) there = pages_there(w.t0 + j + 1);
           const bool edge = k0 + kKeys > inside || pm != all_boxes;
-          if (!(ok = mbar_wait_warp(bar(C::B_SFULL + b), bpar, guard, SITE_TREE_SOFTMAX))) break;
-          tc_fence_after();
           uint32_t seen[GR / 32];  // this row's keys of its group, 32 a word
           if (edge) {
 #pragma unroll
@@ -625,13 +635,9 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::NTHREADS, 1)
               if (boxes == 8) in_page = (in_page & 0xffffu) | ((pm >> (bx + 1)) & 1u ? 0xffff0000u : 0u);  // pages of 16
               seen[i] = live ? m & in_page : 0u;
             }
-            if (k0 + kKeys > inside) {  // the tile holds drafted tokens or rows behind the end
-              if (!(ok = mbar_wait_warp(bar(C::B_FULL + vs_slot), vpar, guard, SITE_TREE_SOFTMAX)) || !(ok = meet()))
-                break;
-              clean_values<D, FP8, GR>(sb + C::OFF_T + vs_slot * C::TILE, row, k0 + row, inside, len,
-                                       c.T > 1 || p.tree != nullptr, group, seen, poison, bad_rows, bad_stage);
-            }
           }
+          if (!(ok = mbar_wait_warp(bar(C::B_SFULL + b), bpar, guard, SITE_TREE_SOFTMAX))) break;
+          tc_fence_after();
           if (warp_live) {
             uint32_t r[GR];
             float s[GR];
@@ -640,14 +646,15 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::NTHREADS, 1)
             tmem_ld_wait<GR>(r);
             // scores in base-2 units, and for each row the largest of what decides the weights' range
             float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-            const uint32_t scales = sb + C::OFF_SCALE + sc * 1536 + group * GR * 4;
+            const float* scales = reinterpret_cast<const float*>(smem + C::OFF_SCALE) + sc * 384 + group * GR;
             if constexpr (FP8) {
 #pragma unroll
               for (int k = 0; k < GR; k += 4) {
-                const uint4 ks = ld_shared_v4(scales + 4 * k);
-                const uint32_t kk[4] = {ks.x, ks.y, ks.z, ks.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) s[k + e] = __uint_as_float(r[k + e]) * rq * __uint_as_float(kk[e]);
+                const float4 ks = *reinterpret_cast<const float4*>(scales + k);
+                const uint64_t a = fmul2(f2pack(__uint_as_float(r[k]), __uint_as_float(r[k + 1])), f2pack(rq, rq));
+                const uint64_t bb = fmul2(f2pack(__uint_as_float(r[k + 2]), __uint_as_float(r[k + 3])), f2pack(rq, rq));
+                f2unpack(fmul2(a, f2pack(ks.x, ks.y)), s[k], s[k + 1]);
+                f2unpack(fmul2(bb, f2pack(ks.z, ks.w)), s[k + 2], s[k + 3]);
               }
             } else {
 #pragma unroll
@@ -664,10 +671,12 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::NTHREADS, 1)
 #pragma unroll
               for (int e = 0; e < 8; ++e) v[e] = s[k + e];
               if constexpr (FP8) {
-                const uint4 a = ld_shared_v4(scales + 1024 + 4 * k), bb = ld_shared_v4(scales + 1024 + 4 * k + 16);
-                v[0] += __uint_as_float(a.x), v[1] += __uint_as_float(a.y), v[2] += __uint_as_float(a.z);
-                v[3] += __uint_as_float(a.w), v[4] += __uint_as_float(bb.x), v[5] += __uint_as_float(bb.y);
-                v[6] += __uint_as_float(bb.z), v[7] += __uint_as_float(bb.w);
+                const float4 a = *reinterpret_cast<const float4*>(scales + 256 + k);
+                const float4 bb = *reinterpret_cast<const float4*>(scales + 256 + k + 4);
+                f2unpack(fadd2(f2pack(v[0], v[1]), f2pack(a.x, a.y)), v[0], v[1]);
+                f2unpack(fadd2(f2pack(v[2], v[3]), f2pack(a.z, a.w)), v[2], v[3]);
+                f2unpack(fadd2(f2pack(v[4], v[5]), f2pack(bb.x, bb.y)), v[4], v[5]);
+                f2unpack(fadd2(f2pack(v[6], v[7]), f2pack(bb.z, bb.w)), v[6], v[7]);
               }
 #pragma unroll
               for (int e = 0; e < 4; ++e) top[e] = fmax3(top[e], v[2 * e], v[2 * e + 1]);
@@ -708,9 +717,8 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::NTHREADS, 1)
             for (int k = 0; k < GR; k += 4) {
               uint64_t vsc[2];
               if constexpr (FP8) {
-                const uint4 a = ld_shared_v4(scales + 512 + 4 * k);
-                vsc[0] = f2pack(__uint_as_float(a.x), __uint_as_float(a.y));
-                vsc[1] = f2pack(__uint_as_float(a.z), __uint_as_float(a.w));
+                const float4 a = *reinterpret_cast<const float4*>(scales + 128 + k);
+                vsc[0] = f2pack(a.x, a.y), vsc[1] = f2pack(a.z, a.w);
               }
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
@@ -757,6 +765,11 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::NTHREADS, 1)
             }
             tmem_st_wait();
           }
+          if (k0 + kKeys > inside) {  // the tile holds drafted tokens or rows behind the end
+            if (!(ok = mbar_wait_warp(bar(C::B_FULL + vs_slot), vpar, guard, SITE_TREE_SOFTMAX)) || !(ok = meet())) break;
+            clean_values<D, FP8, NS>(sb + C::OFF_T + vs_slot * C::TILE, row, k0 + row, inside, len,
+                                     c.T > 1 || p.tree != nullptr, group, seen, poison, bad_rows, bad_stage);
+          }
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(C::B_PFULL + b));
@@ -775,7 +788,7 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::NTHREADS, 1)
         if (at.t0 == 0 && tid == 0) {
           const long long first = lo + mine - at.left;  // the unit's first tile among all tiles
           p.info[static_cast<long long>(at.b) * hms + at.hm] =
-              UnitInfo{static_cast<int>(blockIdx.x), static_cast<int>((first + at.nt - 1) / run)};
+              UnitInfo{static_cast<int>(blockIdx.x), static_cast<int>(quotient(first + at.nt - 1, run))};
         }
         // a NaN score does not move the maximum: where nothing else is seen it is still -inf
         if (lr != lr) ref = lr;
@@ -908,14 +921,19 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::NTHREADS, 1)
         uint4 x[NP];
 #pragma unroll
         for (int k = 0; k < NP; ++k) x[k] = ld_shared_v4(raw + (k * 128 + tid) * 16);
+        int ek = 0, ev = 0;
+        if (kv == 0) {
+          const uint8_t* exps = smem + C::OFF_RAW + rs * C::RAW + 128 * D;
+          ek = exps[tid], ev = exps[128 + tid];
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(C::B_REMPTY + rs));  // the next tile may come while this one is converted
         if (!(ok = mbar_wait_warp(bar(C::B_EMPTY + s), spar, guard, SITE_TREE_CONVERT))) break;
         if (kv == 0) {
           // The tile's scales, for the softmax warps.  This slot held the K tile NSLOT / 2 tiles ago, whose S is
           // done; so the P of NSB tiles before that was used, and the softmax is past it: the NSLOT / 2 + NSB - 1
           // tiles it may still read are not overwritten.
-          const uint8_t* exps = smem + C::OFF_RAW + rs * C::RAW + 128 * D;
           float* scale = reinterpret_cast<float*>(smem + C::OFF_SCALE) + sc * 384 + tid;
-          const int ek = exps[tid], ev = exps[128 + tid];
           // (a row that holds NaN has NaN elements: its scale is 1)
           scale[0] = ek == kExpNaN ? 1.f : __int_as_float(ek << 23);
           scale[128] = ev == kExpNaN ? 1.f : __int_as_float(ev << 23);
@@ -943,10 +961,7 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::NTHREADS, 1)
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(bar(C::B_FULL + s));
-          mbar_arrive(bar(C::B_REMPTY + rs));
-        }
+        if (lane == 0) mbar_arrive(bar(C::B_FULL + s));
         if ((rs += 2) >= C::NRAW) rs -= C::NRAW, rpar ^= 1;
         if ((s += 2) >= C::NSLOT) s -= C::NSLOT, spar ^= 1;
       }
@@ -968,42 +983,72 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::NTHREADS, 1)
   }
 }
 
-// Joins the partial rows of the units that several CTAs share: one warp per row.
+// Joins the partial rows of the units that several CTAs share: one warp per row.  Lane k
+// looks after piece k's sums; the rows of O then come eight pieces at a time.
 template <int D>
 __global__ void __launch_bounds__(128) tree_join_kernel(const __grid_constant__ TreeArgs p, int grid) {
+  constexpr int E = D / 32;  // neighbouring elements of a lane
   pdl_wait();
-  if (*reinterpret_cast<volatile int*>(p.status) != 0) return;  // the kernel before gave up
   const long long unit = blockIdx.x;
   const UnitInfo u = p.info[unit];
+  if (*reinterpret_cast<volatile int*>(p.status) != 0) return;  // the kernel before gave up
   if (u.last <= u.first || u.first < 0 || u.last >= grid) return;  // finished where it was computed
   const int lane = threadIdx.x & 31;
-  const int mt = static_cast<int>(unit % p.M);
+  const int mt = p.M == 1 ? 0 : static_cast<int>(unit % p.M);
   const int n = min(128, p.R - mt * 128);
-  const size_t slot_size = static_cast<size_t>(p.rows) * (D + 3);
+  const size_t slot_size = static_cast<size_t>(p.rows) * (D + 3), sums = static_cast<size_t>(p.rows) * D;
+  auto slot = [&](int k) { return p.part + (2 * static_cast<size_t>(k) + (k == u.first ? 1 : 0)) * slot_size; };
   for (int r = blockIdx.y * 4 + (threadIdx.x >> 5); r < n; r += gridDim.y * 4) {
-    float mx = -INFINITY;
-    for (int k = u.first + lane; k <= u.last; k += 32) {
-      const float* slot = p.part + (2 * static_cast<size_t>(k) + (k == u.first ? 1 : 0)) * slot_size;
-      mx = fmaxf(mx, slot[static_cast<size_t>(p.rows) * D + r]);
-    }
+    float mx = -INFINITY, l = 0.f, lr = 0.f, o[E] = {};
+    for (int k0 = u.first; k0 <= u.last; k0 += 32) {
+      const int k = k0 + lane;
+      float m = -INFINITY, pl = 0.f, plr = 0.f;
+      if (k <= u.last) {
+        const float* at = slot(k) + sums + r;
+        m = at[0], pl = at[p.rows], plr = at[2 * p.rows];
+      }
+      float top = fmaxf(m, mx);
 #pragma unroll
-    for (int m = 16; m > 0; m >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, m));
-    float l = 0.f, lr = 0.f, o[D / 32] = {};
-    for (int k = u.first; k <= u.last; ++k) {
-      const float* slot = p.part + (2 * static_cast<size_t>(k) + (k == u.first ? 1 : 0)) * slot_size;
-      const float* ml = slot + static_cast<size_t>(p.rows) * D;
-      const float m = ml[r];
-      const float f = m == -INFINITY ? 0.f : ex2(m - mx);
-      if (f == 0.f) continue;
-      l = fmaf(f, ml[p.rows + r], l);
-      lr = fmaf(f, ml[2 * p.rows + r], lr);
+      for (int i = 16; i > 0; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
+      const float old = mx == -INFINITY ? 0.f : ex2(mx - top);  // what the pieces so far are worth now
+      const float f = m == -INFINITY ? 0.f : ex2(m - top);
+      pl = f == 0.f ? 0.f : pl * f, plr = f == 0.f ? 0.f : plr * f;
 #pragma unroll
-      for (int e = 0; e < D / 32; ++e) o[e] = fmaf(f, slot[static_cast<size_t>(r) * D + e * 32 + lane], o[e]);
+      for (int i = 16; i > 0; i >>= 1) {
+        pl += __shfl_xor_sync(0xffffffffu, pl, i);
+        plr += __shfl_xor_sync(0xffffffffu, plr, i);
+      }
+      l = l * old + pl, lr = lr * old + plr, mx = top;
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] *= old;
+      const int cnt = min(32, u.last - k0 + 1);
+      for (int i0 = 0; i0 < cnt; i0 += 8) {
+        float v[8][E];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float* at = slot(k0 + min(i0 + i, cnt - 1)) + static_cast<size_t>(r) * D + lane * E;
+#pragma unroll
+          for (int e = 0; e < E; ++e) v[i][e] = at[e];
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float fi = __shfl_sync(0xffffffffu, f, (i0 + i) & 31);
+          if (i0 + i < cnt && fi != 0.f) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[e] = fmaf(fi, v[i][e], o[e]);
+          }
+        }
+      }
     }
-    const size_t grow = (unit / p.M) * p.R + mt * 128 + r;
+    const size_t grow = (p.M == 1 ? unit : unit / p.M) * p.R + mt * 128 + r;
     const float inv = lr == 0.f ? 0.f : 1.f / lr;
-#pragma unroll
-    for (int e = 0; e < D / 32; ++e) p.O[grow * D + e * 32 + lane] = __float2bfloat16_rn(o[e] * inv);
+    __nv_bfloat16* dst = p.O + grow * D + lane * E;
+    if constexpr (E == 4)
+      *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
+    else if constexpr (E == 2)
+      *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(o[0] * inv, o[1] * inv);
+    else
+      *dst = __float2bfloat16_rn(o[0] * inv);
     if (lane == 0) p.L[grow] = lr == 0.f ? -INFINITY : (mx + lg2(l)) * kFwdLn2;
   }
 }
@@ -1023,7 +1068,7 @@ size_t info_bytes(long long units) { return (static_cast<size_t>(units) * sizeof
 
 template <int D, bool FP8, int NS>
 fa_status launch_tree(const TreeArgs& p, const void* Q, int grid, cudaStream_t stream) {
-  using C = TCfg<D, FP8>;
+  using C = TCfg<D, FP8, NS>;
   const CacheView& c = p.c;
   CUtensorMap mQ, mK, mV;
   const int rb = c.page < kKeys ? c.page : kKeys, heads = c.pages * c.Hk;
