@@ -28,16 +28,15 @@ constexpr int kExpNaN = 255;
 constexpr int kExpMin = 27;
 constexpr int kExpMax = 247;  // the scale of the largest bf16 numbers
 
-// Keys of sequence b: its length, clamped to what the table can hold.
-FA_DEV int seq_len(const CacheView& c, int b) {
+// Keys of a sequence: its length, clamped to what the table can hold.
+FA_DEV int clamp_len(const CacheView& c, int n) {
   const int cap = c.cols << c.page_shift;  // at most 2^30 (make_cache_view)
-  return min(max(c.lens[b], 0), cap);
+  return min(max(n, 0), cap);
 }
-FA_DEV int seq_new(const CacheView& c, int b) {
-  if (c.n_new == nullptr) return c.T;
-  const int n = c.n_new[b];
-  return n < 0 ? 0 : n > c.T ? c.T : n;
-}
+FA_DEV int seq_len(const CacheView& c, int b) { return clamp_len(c, c.lens[b]); }
+// New tokens of a sequence.
+FA_DEV int clamp_new(const CacheView& c, int n) { return min(max(n, 0), c.T); }
+FA_DEV int seq_new(const CacheView& c, int b) { return c.n_new == nullptr ? c.T : clamp_new(c, c.n_new[b]); }
 // Position of the first new token (negative when a length is smaller than the number of
 // new tokens: the tokens at negative positions do not exist).
 FA_DEV int seq_prefix(const CacheView& c, int b) { return max(c.lens[b], 0) - seq_new(c, b); }
@@ -46,6 +45,12 @@ FA_DEV int seq_prefix(const CacheView& c, int b) { return max(c.lens[b], 0) - se
 FA_DEV int page_of(const CacheView& c, int b, int j) {
   const int p = c.table[b * c.table_stride + (j >> c.page_shift)];
   return p >= 0 && p < c.pages ? p : -1;
+}
+
+// The table's entry for row j, whatever j is (beyond the table: its last column); to be
+// compared with [0, pages) by the caller.  Needs cols > 0.
+FA_DEV int table_entry(const CacheView& c, int b, int j) {
+  return c.table[b * c.table_stride + min(j >> c.page_shift, c.cols - 1)];
 }
 
 // Host side: checks a cache and a table (fa.h states the rules) and fills the view.

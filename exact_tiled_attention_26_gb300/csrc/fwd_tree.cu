@@ -85,7 +85,8 @@ struct TCfg {
   static constexpr int QX = (128 / NS) * D * 2 + (NS > 1 ? 16384 : 0);
   static constexpr int NRAW = FP8 ? (D == 128 ? (NS == 4 ? 4 : 3) : 6) : 0;    // e4m3 tiles: what fits
   static constexpr int RAW = 128 * D + 256;     // with the exponent bytes of its keys (K tiles: and of their values)
-  static constexpr int NSB = D == 128 ? 2 : 3;  // S / P buffers in tensor memory
+  static constexpr int NSB = 2;                 // S buffers in tensor memory
+  static constexpr int NPB = D == 128 ? 1 : 2;  // P buffers
   static constexpr int NSC = FP8 ? NSLOT / 2 + NSB : 0;  // tiles whose scales are kept (see the converter)
   static constexpr int OFF_T = 0;
   static constexpr int OFF_Q = OFF_T + NSLOT * TILE;
@@ -96,13 +97,15 @@ struct TCfg {
   static constexpr int OFF_BAR = OFF_ROWS + 3 * 128 * 4;
   static constexpr int B_Q = 0, B_QFREE = 1, B_QREADY = 2, B_FULL = 3, B_EMPTY = B_FULL + NSLOT,
                        B_RFULL = B_EMPTY + NSLOT, B_REMPTY = B_RFULL + NRAW, B_SFULL = B_REMPTY + NRAW,
-                       B_PFULL = B_SFULL + NSB, B_PFREE = B_PFULL + NSB, B_OFULL = B_PFREE + NSB, B_OFREE = B_OFULL + 1,
+                       B_SFREE = B_SFULL + NSB, B_PFULL = B_SFREE + NSB, B_PFREE = B_PFULL + NPB, B_OFULL = B_PFREE + NPB, B_OFREE = B_OFULL + 1,
                        B_MEET = B_OFREE + 1, B_SDONE = B_MEET + 1, B_PVDONE = B_SDONE + 1, NBAR = B_PVDONE + 1;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;     // 24 words
   static constexpr int SMEM_USED = OFF_MISC + 96;
   static constexpr int SMEM = (SMEM_USED + 1024 > 120 * 1024) ? SMEM_USED + 1024 : 120 * 1024;
-  // tensor memory columns: S / P buffers, O, Q (two elements a column)
-  static constexpr int TM_S0 = 0, TM_O = NSB * 128, TM_Q = TM_O + D, TM_COLS = 512;
+  // tensor memory columns: S buffers, P buffers and Q (two elements a column), O.  P has its own columns, so that
+  // an S buffer is free again as soon as its scores are in registers: with P written over S the loop
+  // softmax - P V - S - softmax bound the kernel (2 buffers: 2040 cycles a tile at d = 128).
+  static constexpr int TM_S0 = 0, TM_P0 = NSB * 128, TM_O = TM_P0 + NPB * 64, TM_Q = TM_O + D, TM_COLS = 512;
   static constexpr int NTHREADS = FP8 ? 512 : 256;
   static_assert(SMEM <= 232448, "shared memory budget");
   static_assert(TM_Q + D / 2 <= TM_COLS, "tensor memory budget");
@@ -320,28 +323,13 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
   const int hms = c.Hk * p.M;
 
   pdl_trigger();  // the joining kernel may be made ready now; it waits for this one's end
-  if (threadIdx.x == 0) {
-    mbar_init(bar(C::B_Q), 1);
-    mbar_init(bar(C::B_QFREE), 4);
-    mbar_init(bar(C::B_QREADY), 4);
-    for (int i = 0; i < C::NSLOT; ++i) {
-      mbar_init(bar(C::B_FULL + i), FP8 ? 4 : 1);
-      mbar_init(bar(C::B_EMPTY + i), 1);
-    }
-    for (int i = 0; i < C::NRAW; ++i) {
-      mbar_init(bar(C::B_RFULL + i), 1);
-      mbar_init(bar(C::B_REMPTY + i), 4);
-    }
-    for (int i = 0; i < C::NSB; ++i) {
-      mbar_init(bar(C::B_SFULL + i), 1);
-      mbar_init(bar(C::B_PFULL + i), 4);
-      mbar_init(bar(C::B_PFREE + i), 1);
-    }
-    mbar_init(bar(C::B_OFULL), 1);
-    mbar_init(bar(C::B_OFREE), 4);
-    mbar_init(bar(C::B_MEET), 4);
-    mbar_init(bar(C::B_SDONE), 1);
-    mbar_init(bar(C::B_PVDONE), 1);
+  if (threadIdx.x < C::NBAR) {
+    const int i = threadIdx.x;
+    // one arrival for loads and commits, one for each of four warps elsewhere
+    const bool four = i == C::B_QFREE || i == C::B_QREADY || i == C::B_OFREE || i == C::B_MEET ||
+                      (i >= C::B_SFREE && i < C::B_PFREE) || (FP8 && i >= C::B_FULL && i < C::B_EMPTY) ||
+                      (i >= C::B_REMPTY && i < C::B_SFULL);
+    mbar_init(bar(i), four ? 4 : 1);
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -403,14 +391,10 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
       constexpr int NR = FP8 ? C::NRAW : C::NSLOT, BFULL = FP8 ? C::B_RFULL : C::B_FULL,
                     BEMPTY = FP8 ? C::B_REMPTY : C::B_EMPTY;
       for (; ok && w.more(); ++seg) {
-        const int len = seq_len(c, w.b), h = w.hm / p.M, mt = w.hm - h * p.M;
+        const int len = seq_len(c, w.b), h = p.M == 1 ? w.hm : w.hm / p.M, mt = w.hm - h * p.M;
         const int n = w.n();
-        auto where = [&](int tile) {  // z coordinate of this lane's box
-          const int j = tile * kKeys + pi * rb;
-          const int page = issues && j < len ? page_of(c, w.b, j) : -1;
-          return page < 0 ? nowhere : page * c.Hk + h;
-        };
-        int z = where(w.t0);
+        auto entry = [&](int tile) { return table_entry(c, w.b, tile * kKeys + pi * rb); };
+        int next = entry(w.t0);  // loaded a tile ahead, looked at when used
         // the softmax warps have taken the Q before it
         if (seg > 0 && !(ok = mbar_wait_warp(bar(C::B_QFREE), (seg - 1) & 1, guard, SITE_TREE_PRODUCER))) break;
         if (lane == 0) {
@@ -421,7 +405,9 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
         for (int j = 0; ok && j < n; ++j) {
           const int tile = w.t0 + j;
           const int y = (tile * kKeys + pi * rb) & (c.page - 1);
-          const int zn = j + 1 < n ? where(tile + 1) : 0;
+          // this lane's box: z coordinate of its page and head
+          const int z = issues && tile * kKeys + pi * rb < len && next >= 0 && next < c.pages ? next * c.Hk + h : nowhere;
+          if (j + 1 < n) next = entry(tile + 1);
           for (int kv = 0; kv < 2; ++kv) {
             if (!(ok = mbar_wait_warp(bar(BEMPTY + slot), parity, guard, SITE_TREE_PRODUCER))) break;
             const uint32_t full = bar(BFULL + slot);
@@ -454,7 +440,6 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
             ++items;
             if (++slot == NR) slot = 0, parity ^= 1;
           }
-          z = zn;
         }
         w.next(c, hms);
       }
@@ -474,8 +459,8 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
         const int n = w.n();
         if (!(ok = mbar_wait(bar(C::B_QREADY), seg & 1, guard, SITE_TREE_MMA))) break;
         for (int j = 0; j < n; ++j) {
-          // S buffer b last held P of an earlier tile: the product that read it is done
-          if (!(ok = mbar_wait(bar(C::B_PFREE + b), bpar, guard, SITE_TREE_MMA))) break;
+          // the scores that were in S buffer b have been read
+          if (!(ok = mbar_wait(bar(C::B_SFREE + b), bpar, guard, SITE_TREE_MMA))) break;
           if (!(ok = mbar_wait(bar(C::B_FULL + s), spar, guard, SITE_TREE_MMA))) break;
           tc_fence_after();
           const uint32_t kb = sb + C::OFF_T + s * C::TILE;
@@ -505,13 +490,13 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
           // a unit's first product overwrites O: the epilogue before it has read it
           if (j == 0 && seg > 0 && !(ok = mbar_wait(bar(C::B_OFREE), (seg - 1) & 1, guard, SITE_TREE_MMA))) break;
           tc_fence_after();
-          const uint32_t vb = sb + C::OFF_T + s * C::TILE, aP = tmem + C::TM_S0 + b * 128;
+          const uint32_t vb = sb + C::OFF_T + s * C::TILE, aP = tmem + C::TM_P0 + b * 64;
 #pragma unroll
           for (int ks = 0; ks < kKeys / 16; ++ks)
             mma_ts(tmem + C::TM_O, aP + ks * 8, sdesc_mnmajor<C::SWB, 128>(vb, ks), idO, (j > 0 || ks > 0));
           mma_commit(bar(C::B_EMPTY + s));
           mma_commit(bar(C::B_PFREE + b));
-          if (++b == C::NSB) b = 0, bpar ^= 1;
+          if (++b == C::NPB) b = 0, bpar ^= 1;
           if ((s += 2) >= C::NSLOT) s -= C::NSLOT, spar ^= 1;
         }
         if (!ok) break;
@@ -533,8 +518,8 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
       const int boxes = c.page < kKeys ? kKeys / c.page : 1;
       const uint32_t all_boxes = boxes == 1 ? 1u : (1u << boxes) - 1u;
       bool ok = true;
-      int seg = 0, b = 0, vs_slot = 1, sc = 0;  // S buffer, slot of V, scales
-      uint32_t bpar = 0, vpar = 0, meet_parity = 0;
+      int seg = 0, b = 0, pb = 0, vs_slot = 1, sc = 0;  // S buffer, P buffer, slot of V, scales
+      uint32_t bpar = 0, pfree = 1, vpar = 0, meet_parity = 0;
       // The four softmax warps meet; a wait with a limit.  It does not look at the abort flag, so that
       // either all four pass or none does, and what follows may use plain barriers.
       auto meet = [&]() -> bool {
@@ -596,12 +581,28 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
         }
         return true;
       };
+      // The other groups' weights are zero, for good: a tile writes its own group's columns only.
+      if constexpr (NS > 1) {
+        uint32_t zero[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) zero[k] = 0u;
+#pragma unroll
+        for (int k = 0; k < C::NPB * 4; ++k) tmem_st16(tl + C::TM_P0 + 16 * k, zero);
+      }
       ok = take_q(0);
+      // What a unit starts with is loaded before the epilogue of the one before it
+      // (as it is in memory, so that the loads are all under way at once).
+      auto new_of = [&](int i) { return c.n_new == nullptr ? c.T : c.n_new[i]; };
+      int raw_len = c.lens[w.b], raw_new = new_of(w.b);
+      auto page_entry = [&](int tile) {  // this lane's box
+        return table_entry(c, w.b, tile * kKeys + (lane < boxes ? lane : 0) * (kKeys / boxes));
+      };
+      int entry = page_entry(w.t0);
       for (; ok && w.more(); ++seg) {
         const int n = w.n();
-        const int h = w.hm / p.M, mt = w.hm - h * p.M;
+        const int h = p.M == 1 ? w.hm : w.hm / p.M, mt = w.hm - h * p.M;
         const int q = mt * 128 + r_in, t = q % c.T;
-        const int len = seq_len(c, w.b), nn = seq_new(c, w.b), prefix = seq_prefix(c, w.b);
+        const int len = clamp_len(c, raw_len), nn = clamp_new(c, raw_new), prefix = max(raw_len, 0) - nn;
         const int inside = min(prefix, len);  // keys below it are seen by every live row
         const bool live = q < p.R && t < nn;  // rows that are not there see nothing
         const bool warp_live = mt * 128 + (wq * 32) % GR < p.R;
@@ -612,15 +613,12 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
         Poison<D> poison;
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) poison.pos[i] = poison.neg[i] = 0u;
-        auto pages_there = [&](int tile) {  // bit i: box i's page exists (this lane's load, for the ballot)
-          const int j = tile * kKeys + lane * (kKeys / boxes);
-          return lane < boxes && j < len && page_of(c, w.b, j) >= 0;
-        };
-        bool there = pages_there(w.t0);
         for (int j = 0; j < n; ++j) {
           const int k0 = (w.t0 + j) * kKeys;
-          const uint32_t pm = __ballot_sync(0xffffffffu, there);
-          if (j + 1 < n) there = pages_there(w.t0 + j + 1);
+          // bit i: box i's page exists
+          const uint32_t pm = __ballot_sync(0xffffffffu, lane < boxes && k0 + lane * (kKeys / boxes) < len && entry >= 0 &&
+                                                             entry < c.pages);
+          if (j + 1 < n) entry = page_entry(w.t0 + j + 1);
           const bool edge = k0 + kKeys > inside || pm != all_boxes;
           uint32_t seen[GR / 32];  // this row's keys of its group, 32 a word
           if (edge) {
@@ -644,6 +642,9 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
 #pragma unroll
             for (int i = 0; i < GR / 32; ++i) tmem_ld32(tl + C::TM_S0 + b * 128 + group * GR + 32 * i, r + 32 * i);
             tmem_ld_wait<GR>(r);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(C::B_SFREE + b));
             // scores in base-2 units, and for each row the largest of what decides the weights' range
             float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
             const float* scales = reinterpret_cast<const float*>(smem + C::OFF_SCALE) + sc * 384 + group * GR;
@@ -692,9 +693,11 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
                 const float new_ref = tile_top + kStart;
                 const float alpha = move ? ex2(ref - new_ref) : 1.f;
                 if (move) l *= alpha, lr *= alpha, ref = new_ref;
-                // the product that last wrote O is done: it read the S buffer before this one
-                const int pb = b == 0 ? C::NSB - 1 : b - 1;
-                if (!(ok = mbar_wait_warp(bar(C::B_PFREE + pb), b == 0 ? bpar ^ 1 : bpar, guard, SITE_TREE_SOFTMAX))) break;
+                // the product that last wrote O is done
+                const int last = pb == 0 ? C::NPB - 1 : pb - 1;
+                if (!(ok = mbar_wait_warp(bar(C::B_PFREE + last), C::NPB == 1 || pb != 0 ? pfree ^ (C::NPB > 1) : pfree, guard,
+                                          SITE_TREE_SOFTMAX)))
+                  break;
                 tc_fence_after();
 #pragma unroll 1
                 for (int i = 0; i < D / 32; ++i) {
@@ -743,27 +746,20 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
             l += a0 + a1;
             // bf16 weights are normalised by their own sum; f16 ones are off by 2^-11 at most
             lr = FP8 ? l : lr + (rl[0] + rl[1]) + (rh[0] + rh[1]);
-            // own keys' weights, zeros for the other groups'
+            // the product that read this P buffer is done
+            if (!(ok = mbar_wait_warp(bar(C::B_PFREE + pb), pfree, guard, SITE_TREE_SOFTMAX))) break;
+            tc_fence_after();
+            const uint32_t own = tl + C::TM_P0 + pb * 64 + group * (GR / 2);
+            if constexpr (NS == 4) tmem_st16(own, pk);
+            if constexpr (NS == 2) tmem_st32(own, pk);
             if constexpr (NS == 1) {
-              tmem_st32(tl + C::TM_S0 + b * 128, pk);
-              tmem_st32(tl + C::TM_S0 + b * 128 + 32, pk + 32);
-            } else {
-              uint32_t zero[GR / 2];
-#pragma unroll
-              for (int k = 0; k < GR / 2; ++k) zero[k] = 0u;
-#pragma unroll
-              for (int g = 0; g < NS; ++g) {
-                const uint32_t at = tl + C::TM_S0 + b * 128 + g * (GR / 2);
-                if (g == group) {
-                  if constexpr (NS == 2) tmem_st32(at, pk);
-                  else tmem_st16(at, pk);
-                } else {
-                  if constexpr (NS == 2) tmem_st32(at, zero);
-                  else tmem_st16(at, zero);
-                }
-              }
+              tmem_st32(own, pk);
+              tmem_st32(own + 32, pk + 32);
             }
             tmem_st_wait();
+          } else {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(C::B_SFREE + b));
           }
           if (k0 + kKeys > inside) {  // the tile holds drafted tokens or rows behind the end
             if (!(ok = mbar_wait_warp(bar(C::B_FULL + vs_slot), vpar, guard, SITE_TREE_SOFTMAX)) || !(ok = meet())) break;
@@ -772,8 +768,9 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
           }
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar(C::B_PFULL + b));
+          if (lane == 0) mbar_arrive(bar(C::B_PFULL + pb));
           if (++b == C::NSB) b = 0, bpar ^= 1;
+          if (++pb == C::NPB) pb = 0, pfree ^= 1;
           if ((vs_slot += 2) >= C::NSLOT) vs_slot -= C::NSLOT, vpar ^= 1;
           if (FP8 && ++sc == C::NSC) sc = 0;
         }
@@ -781,7 +778,10 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
         // ------------------------------------------------------------ this run's part of the unit is done
         const Walk at = w;
         w.next(c, hms);
-        if (w.more() && !(ok = take_q(seg + 1))) break;  // the next unit's S may be formed meanwhile
+        if (w.more()) {
+          raw_len = c.lens[w.b], raw_new = new_of(w.b), entry = page_entry(w.t0);
+          if (!(ok = take_q(seg + 1))) break;  // the next unit's S may be formed meanwhile
+        }
         if (!(ok = mbar_wait_warp(bar(C::B_OFULL), seg & 1, guard, SITE_TREE_SOFTMAX)) || !(ok = meet())) break;
         tc_fence_after();
         const bool whole = at.t0 == 0 && n == at.nt;
@@ -793,41 +793,12 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
         // a NaN score does not move the maximum: where nothing else is seen it is still -inf
         if (lr != lr) ref = lr;
         if (!live) ref = -INFINITY, l = lr = 0.f;  // whatever its lane computed
-        float f = 1.f;  // this group's share in the row's common reference
-        float om = ref, ol = l, olr = lr;
-        const int orow = tid / NS, opart = tid % NS;  // the row this thread stores its share of
-        if constexpr (NS > 1) {
-          rows[row] = ref;
-          rows[128 + row] = l;
-          rows[256 + row] = lr;
-          named_bar_sync(1, 128);
-          float mx = -INFINITY;
-          om = -INFINITY, ol = olr = 0.f;
-#pragma unroll
-          for (int g = 0; g < NS; ++g) {
-            mx = fmaxf(mx, rows[g * GR + r_in]);
-            om = fmaxf(om, rows[g * GR + orow]);
-          }
-          f = ref == -INFINITY ? 0.f : ex2(ref - mx);
-#pragma unroll
-          for (int g = 0; g < NS; ++g) {
-            const float mg = rows[g * GR + orow];
-            const float fg = mg == -INFINITY ? 0.f : ex2(mg - om);
-            ol += fg * rows[128 + g * GR + orow];
-            olr += fg * rows[256 + g * GR + orow];
-          }
-          if (olr != olr) om = olr;  // so that the join keeps the row
-        }
-        const int oq = mt * 128 + orow;
-        const bool store = oq < p.R;
-        const size_t grow = (static_cast<size_t>(at.b) * c.Hk + h) * p.R + oq;
         float* slot = p.part + (2 * static_cast<size_t>(blockIdx.x) + (at.t0 == 0 ? 1 : 0)) * p.rows * (D + 3);
-        const float inv = olr == 0.f ? 0.f : 1.f / olr;
-        // 32 columns at a time (a loop, not unrolled: this code runs once per unit, and fetching it costs more
-        // than the jumps)
-#pragma unroll 1
-        for (int i = 0; i < D / 32; ++i) {
-          uint32_t o[32];
+        float* sums = slot + static_cast<size_t>(p.rows) * D;
+        const size_t row0 = (static_cast<size_t>(at.b) * c.Hk + h) * p.R + mt * 128;  // the query tile's first row
+        // 32 columns of this thread's O at a time.  Loops stay loops: the code runs once per unit, and fetching
+        // unrolled code costs more than running it.
+        auto load_o = [&](int i, uint32_t (&o)[32]) {
           tmem_ld32(tl + C::TM_O + 32 * i, o);
           tmem_ld_wait<32>(o);
           uint32_t pp = 0, pn = 0;
@@ -843,66 +814,120 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
                                        (a && d ? __int_as_float(0x7fffffff) : a ? INFINITY : -INFINITY));
             }
           }
-          constexpr int CPT = 8 / NS;  // 16-byte pieces of the 32 columns that a thread stores
-          float a[4 * CPT];
-          if constexpr (NS == 1) {
+        };
+        if constexpr (NS == 1) {
+          const int wrow = wq * 32, nvalid = p.R - mt * 128 - wrow;  // the warp's rows, stored whole rows at a time
+          const float inv = lr == 0.f ? 0.f : 1.f / lr;
+#pragma unroll 1
+          for (int i = 0; i < D / 32; ++i) {
+            uint32_t o[32];
+            load_o(i, o);
 #pragma unroll
-            for (int k = 0; k < 32; ++k) a[k] = lr == 0.f ? 0.f : __uint_as_float(o[k]);
-          } else {
-            if (i > 0) named_bar_sync(1, 128);  // the columns before have been read
+            for (int e = 0; e < 32; ++e) o[e] = lr == 0.f ? 0u : o[e];
+            if (whole) {
+              uint32_t pk[16];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              float4 v;
-              v.x = f == 0.f ? 0.f : __uint_as_float(o[4 * k]) * f;
-              v.y = f == 0.f ? 0.f : __uint_as_float(o[4 * k + 1]) * f;
-              v.z = f == 0.f ? 0.f : __uint_as_float(o[4 * k + 2]) * f;
-              v.w = f == 0.f ? 0.f : __uint_as_float(o[4 * k + 3]) * f;
-              xch[row * 8 + (k ^ (row & 7))] = v;
+              for (int e = 0; e < 16; ++e)
+                pk[e] = pack_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+              warp_store_rows<4, 0>(pk, reinterpret_cast<uint8_t*>(p.O + (row0 + wrow) * D + 32 * i), D * 2, nvalid, lane);
+            } else {
+              warp_store_rows<8, 0>(o, reinterpret_cast<uint8_t*>(slot + static_cast<size_t>(wrow) * D + 32 * i), D * 4,
+                                    nvalid, lane);
+            }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(C::B_OFREE));
+          if (lane < nvalid) {
+            if (whole) p.L[row0 + row] = lr == 0.f ? -INFINITY : (ref + lg2(l)) * kFwdLn2;
+            else sums[row] = ref, sums[p.rows + row] = l, sums[2 * p.rows + row] = lr;
+          }
+        } else {
+          // The groups' rows are added up through shared memory, XR rows at a time: every thread then has EPT
+          // elements of one of them.
+          constexpr int XR = 16384 / (NS * D * 4), TPR = 128 / XR, EPT = D / TPR;
+          static_assert(EPT == 8 * (4 / NS) || EPT >= 8, "whole 16-byte pieces");
+          rows[row] = ref;
+          rows[128 + row] = l;
+          rows[256 + row] = lr;
+          named_bar_sync(1, 128);
+          float mx = -INFINITY;
+#pragma unroll
+          for (int g = 0; g < NS; ++g) mx = fmaxf(mx, rows[g * GR + r_in]);
+          const float f = ref == -INFINITY ? 0.f : ex2(ref - mx);  // this group's share in the row's common reference
+          const int n_rows = min(GR, p.R - mt * 128);
+#pragma unroll 1
+          for (int x0 = 0; x0 < n_rows; x0 += XR) {
+            if (x0 > 0) named_bar_sync(1, 128);  // the rows before have been read
+            const int xr = r_in - x0;
+            const bool mine_now = xr >= 0 && xr < XR;
+            if (__any_sync(0xffffffffu, mine_now)) {
+              float4* dst = xch + (group * XR + (xr & (XR - 1))) * (D / 4);
+#pragma unroll 1
+              for (int i = 0; i < D / 32; ++i) {
+                uint32_t o[32];
+                load_o(i, o);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                  float4 v;
+                  v.x = f == 0.f ? 0.f : __uint_as_float(o[4 * k]) * f;
+                  v.y = f == 0.f ? 0.f : __uint_as_float(o[4 * k + 1]) * f;
+                  v.z = f == 0.f ? 0.f : __uint_as_float(o[4 * k + 2]) * f;
+                  v.w = f == 0.f ? 0.f : __uint_as_float(o[4 * k + 3]) * f;
+                  if (mine_now) dst[8 * i + (k ^ (xr & 7))] = v;
+                }
+              }
+            }
+            if (x0 + XR >= n_rows) {  // O has been read
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(bar(C::B_OFREE));
             }
             named_bar_sync(1, 128);
+            const int orow = x0 + tid / TPR, part = tid % TPR;
+            if (orow < n_rows) {
+              float om = -INFINITY, ol = 0.f, olr = 0.f;
 #pragma unroll
-            for (int k = 0; k < CPT; ++k) {
-              const int piece = opart * CPT + k;
-              float4 v = xch[orow * 8 + (piece ^ (orow & 7))];
+              for (int g = 0; g < NS; ++g) om = fmaxf(om, rows[g * GR + orow]);
 #pragma unroll
-              for (int g = 1; g < NS; ++g) {
-                const float4 y = xch[(g * GR + orow) * 8 + (piece ^ ((g * GR + orow) & 7))];
-                v.x += y.x, v.y += y.y, v.z += y.z, v.w += y.w;
+              for (int g = 0; g < NS; ++g) {
+                const float mg = rows[g * GR + orow];
+                const float fg = mg == -INFINITY ? 0.f : ex2(mg - om);
+                ol += fg * rows[128 + g * GR + orow];
+                olr += fg * rows[256 + g * GR + orow];
               }
-              a[4 * k] = v.x, a[4 * k + 1] = v.y, a[4 * k + 2] = v.z, a[4 * k + 3] = v.w;
+              if (olr != olr) om = olr;  // so that the join keeps the row
+              float a[EPT];
+#pragma unroll
+              for (int k = 0; k < EPT / 4; ++k) {
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int g = 0; g < NS; ++g) {
+                  const float4 y = xch[(g * XR + tid / TPR) * (D / 4) + ((part * (EPT / 4) + k) ^ ((tid / TPR) & 7))];
+                  v.x += y.x, v.y += y.y, v.z += y.z, v.w += y.w;
+                }
+                a[4 * k] = v.x, a[4 * k + 1] = v.y, a[4 * k + 2] = v.z, a[4 * k + 3] = v.w;
+              }
+              const float inv = olr == 0.f ? 0.f : 1.f / olr;
+              if (whole) {
+                uint4* dst = reinterpret_cast<uint4*>(p.O + (row0 + orow) * D + part * EPT);
+#pragma unroll
+                for (int k = 0; k < EPT / 8; ++k)
+                  dst[k] = make_uint4(pack_bf16x2(a[8 * k] * inv, a[8 * k + 1] * inv),
+                                      pack_bf16x2(a[8 * k + 2] * inv, a[8 * k + 3] * inv),
+                                      pack_bf16x2(a[8 * k + 4] * inv, a[8 * k + 5] * inv),
+                                      pack_bf16x2(a[8 * k + 6] * inv, a[8 * k + 7] * inv));
+                if (part == 0) p.L[row0 + orow] = olr == 0.f ? -INFINITY : (om + lg2(ol)) * kFwdLn2;
+              } else {
+                float4* dst = reinterpret_cast<float4*>(slot + static_cast<size_t>(orow) * D + part * EPT);
+#pragma unroll
+                for (int k = 0; k < EPT / 4; ++k) dst[k] = make_float4(a[4 * k], a[4 * k + 1], a[4 * k + 2], a[4 * k + 3]);
+                if (part == 0) sums[orow] = om, sums[p.rows + orow] = ol, sums[2 * p.rows + orow] = olr;
+              }
             }
           }
-          if (store) {
-            const int col = 32 * i + opart * CPT * 4;
-            if (whole) {
-              uint4* dst = reinterpret_cast<uint4*>(p.O + grow * D + col);
-#pragma unroll
-              for (int k = 0; k < CPT / 2; ++k)
-                dst[k] = make_uint4(pack_bf16x2(a[8 * k] * inv, a[8 * k + 1] * inv),
-                                    pack_bf16x2(a[8 * k + 2] * inv, a[8 * k + 3] * inv),
-                                    pack_bf16x2(a[8 * k + 4] * inv, a[8 * k + 5] * inv),
-                                    pack_bf16x2(a[8 * k + 6] * inv, a[8 * k + 7] * inv));
-            } else {
-              float4* dst = reinterpret_cast<float4*>(slot + static_cast<size_t>(orow) * D + col);
-#pragma unroll
-              for (int k = 0; k < CPT; ++k) dst[k] = make_float4(a[4 * k], a[4 * k + 1], a[4 * k + 2], a[4 * k + 3]);
-            }
-          }
+          named_bar_sync(1, 128);  // rows and the exchange are free again
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(C::B_OFREE));
-        if (store && opart == 0) {
-          if (whole) {
-            p.L[grow] = olr == 0.f ? -INFINITY : (om + lg2(ol)) * kFwdLn2;
-          } else {
-            float* ml = slot + static_cast<size_t>(p.rows) * D;
-            ml[orow] = om;
-            ml[p.rows + orow] = ol;
-            ml[2 * p.rows + orow] = olr;
-          }
-        }
-        if constexpr (NS > 1) named_bar_sync(1, 128);  // rows and the exchange are free again
       }
     }
   } else if constexpr (FP8) {
@@ -912,6 +937,17 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
       // Warps 8..11 take the K tiles, 12..15 the V tiles: two tiles under way at once.
       const int kv = (warp - 8) >> 2, tid = (threadIdx.x - 256) & 127;
       constexpr int PPR = D / 16, NP = PPR;  // 16-byte pieces of an e4m3 row; of a thread
+      // Piece `sub` of rows k * ROWS + row, k < NP.  Eight lanes read 128 bytes of different banks and write 16-byte
+      // units of different banks: at d = 128 (two chunks, 8 pieces a row) lanes 4..7 of eight take the upper half of
+      // the neighbouring row, whose swizzle differs in the lowest bit.
+      constexpr int ROWS = 128 / PPR;
+      const int sub = tid % PPR;
+      const int row = PPR == 8 ? (tid >> 4) * 2 + (((tid >> 2) ^ (tid >> 3)) & 1) : tid / PPR;
+      const uint32_t sw = swz_row<C::SWB>(row);
+      const uint32_t u0 = sub * 16 % C::CE / 8;
+      const uint32_t to = (sub * 16 / C::CE) * (128 * C::SWB) + row * C::SWB;
+      const uint32_t to0 = to + ((u0 ^ sw) << 4), to1 = to + (((u0 + 1) ^ sw) << 4);
+      static_assert(ROWS % 8 == 0, "steps keep the swizzle");
       bool ok = true;
       int rs = kv % C::NRAW, s = kv, sc = 0;  // slots of the rings
       uint32_t rpar = 0, spar = 1;
@@ -920,7 +956,7 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
         const uint32_t raw = sb + C::OFF_RAW + rs * C::RAW, dst = sb + C::OFF_T + s * C::TILE;
         uint4 x[NP];
 #pragma unroll
-        for (int k = 0; k < NP; ++k) x[k] = ld_shared_v4(raw + (k * 128 + tid) * 16);
+        for (int k = 0; k < NP; ++k) x[k] = ld_shared_v4(raw + (k * ROWS + row) * D + sub * 16);
         int ek = 0, ev = 0;
         if (kv == 0) {
           const uint8_t* exps = smem + C::OFF_RAW + rs * C::RAW + 128 * D;
@@ -942,7 +978,6 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
         }
 #pragma unroll
         for (int k = 0; k < NP; ++k) {
-          const int piece = k * 128 + tid, row = piece / PPR, sub = piece % PPR;
           const uint32_t w4[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
           uint32_t o[8];
 #pragma unroll
@@ -950,14 +985,8 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
             o[2 * q] = e4m3x2_to_f16x2(w4[q] & 0xffffu);
             o[2 * q + 1] = e4m3x2_to_f16x2(w4[q] >> 16);
           }
-          // the row's 16-byte units 2 sub and 2 sub + 1; lanes of the upper half of a wide row
-          // write them in the other order, so that 8 lanes always hit 8 different units
-          const bool flip = (sub * 2 / (C::CE / 8)) & 1;
-          const uint32_t base = dst + (sub * 16 / C::CE) * (128 * C::SWB) + row * C::SWB;
-          const uint32_t u0 = sub * 16 % C::CE / 8, sw = swz_row<C::SWB>(row);
-          const uint4 lo4 = make_uint4(o[0], o[1], o[2], o[3]), hi4 = make_uint4(o[4], o[5], o[6], o[7]);
-          st_shared_v4(base + (((u0 + (flip ? 1 : 0)) ^ sw) << 4), flip ? hi4 : lo4);
-          st_shared_v4(base + (((u0 + (flip ? 0 : 1)) ^ sw) << 4), flip ? lo4 : hi4);
+          st_shared_v4(dst + to0 + k * ROWS * C::SWB, make_uint4(o[0], o[1], o[2], o[3]));
+          st_shared_v4(dst + to1 + k * ROWS * C::SWB, make_uint4(o[4], o[5], o[6], o[7]));
         }
         fence_proxy_async_smem();
         __syncwarp();
