@@ -23,9 +23,11 @@
 // share a tile's exponentials even for a single query row; the groups' results are
 // joined at the end of a unit like the partial rows of different CTAs.
 //
-// Per CTA: warp 0 loads Q and a ring of K and V tiles (TMA boxes of one page each, one
-// per lane); warp 1 issues S = Q K^T, warp 2 O += P V (tcgen05; Q, P and the accumulators in
-// tensor memory); warps 4..7 put Q there, run the softmax and the epilogue.
+// Per CTA: warps 0 and 3 load a ring of K and V tiles (TMA boxes of one page each;
+// issuing a tile's boxes takes about as long as its bytes, so K and V each have a warp);
+// warp 1 issues S = Q K^T, warp 2 O += P V (tcgen05; Q, P and the accumulators in
+// tensor memory); warps 4..7 put Q there, run the
+// softmax and the epilogue.
 //
 // An e4m3 cache arrives in a ring of its own; warps 8..15 turn its tiles into f16 tiles
 // (one instruction for two elements, exact) and Q is scaled to f16 row by row.  The
@@ -51,6 +53,7 @@ namespace {
 
 constexpr int kMaxGrid = 152;  // CTAs at most, one per SM
 constexpr int kKeys = 128;     // keys per tile
+constexpr int kUnitCost = 3;   // see Walk
 
 enum : int { SITE_TREE_PRODUCER = 0x501, SITE_TREE_MMA = 0x502, SITE_TREE_SOFTMAX = 0x503, SITE_TREE_CONVERT = 0x504 };
 
@@ -62,6 +65,7 @@ struct UnitInfo {
 
 struct TreeArgs {
   CacheView c;
+  const __nv_bfloat16* Q;
   __nv_bfloat16* O;
   float* L;
   const unsigned long long* tree;  // [.., T, words], or null
@@ -78,24 +82,22 @@ template <int D, bool FP8, int NS>
 struct TCfg {
   static constexpr int SWB = (D * 2 >= 128) ? 128 : D * 2;
   static constexpr int CE = SWB / 2;
-  static constexpr int NCH = D / CE;
   static constexpr int TILE = 128 * D * 2;
   static constexpr int NSLOT = FP8 ? (D == 128 ? 4 : 6) : (D == 128 ? 6 : 8);  // 16-bit tiles, K and V in turn
-  // Q (128 / NS rows) and, for NS > 1, 16 KB of the epilogue's exchange
-  static constexpr int QX = (128 / NS) * D * 2 + (NS > 1 ? 16384 : 0);
-  static constexpr int NRAW = FP8 ? (D == 128 ? (NS == 4 ? 4 : 3) : 6) : 0;    // e4m3 tiles: what fits
+  static constexpr int NRAW = FP8 ? (D == 128 ? 4 : 6) : 0;  // e4m3 tiles
+  // K tiles use the even slots of a ring and V tiles the odd ones, each with a producer and a consumer of its own.
+  static_assert(NSLOT % 2 == 0 && NRAW % 2 == 0, "disjoint slots");
   static constexpr int RAW = 128 * D + 256;     // with the exponent bytes of its keys (K tiles: and of their values)
   static constexpr int NSB = 2;                 // S buffers in tensor memory
   static constexpr int NPB = D == 128 ? 1 : 2;  // P buffers
   static constexpr int NSC = FP8 ? NSLOT / 2 + NSB : 0;  // tiles whose scales are kept (see the converter)
   static constexpr int OFF_T = 0;
-  static constexpr int OFF_Q = OFF_T + NSLOT * TILE;
-  static constexpr int OFF_X = OFF_Q + (128 / NS) * D * 2;
-  static constexpr int OFF_RAW = OFF_Q + QX;
+  static constexpr int OFF_X = OFF_T + NSLOT * TILE;      // the epilogue's exchange
+  static constexpr int OFF_RAW = OFF_X + (NS > 1 ? 16384 : 0);
   static constexpr int OFF_SCALE = OFF_RAW + NRAW * RAW;  // [NSC][3][128] floats: 2^k of K, 2^k of V, k of V
   static constexpr int OFF_ROWS = OFF_SCALE + NSC * 3 * 128 * 4;  // [3][128] floats
   static constexpr int OFF_BAR = OFF_ROWS + 3 * 128 * 4;
-  static constexpr int B_Q = 0, B_QFREE = 1, B_QREADY = 2, B_FULL = 3, B_EMPTY = B_FULL + NSLOT,
+  static constexpr int B_QREADY = 0, B_FULL = 1, B_EMPTY = B_FULL + NSLOT,
                        B_RFULL = B_EMPTY + NSLOT, B_REMPTY = B_RFULL + NRAW, B_SFULL = B_REMPTY + NRAW,
                        B_SFREE = B_SFULL + NSB, B_PFULL = B_SFREE + NSB, B_PFREE = B_PFULL + NPB, B_OFULL = B_PFREE + NPB, B_OFREE = B_OFULL + 1,
                        B_MEET = B_OFREE + 1, B_SDONE = B_MEET + 1, B_PVDONE = B_SDONE + 1, NBAR = B_PVDONE + 1;
@@ -123,19 +125,23 @@ FA_DEV long long quotient(long long a, long long b) {
   return a / b;
 }
 
-// A CTA's run of tiles, unit by unit.
+// A CTA's run.  The units stand one after the other on a line, each with kUnitCost places
+// (what starting and ending a unit costs, in tiles) before its tiles, and the CTAs take
+// equal runs of places: those with a unit's border in them get that many tiles less.
 struct Walk {
   int b, hm, t0, nt;  // sequence, key head and row tile (h * M + mt), first tile, tiles of the unit
-  long long left;     // tiles of the run from here on
-  FA_DEV bool more() const { return left > 0; }
-  FA_DEV int n() const { return nt - t0 < left ? nt - t0 : static_cast<int>(left); }
+  int cost;           // places before the first tile
+  long long left;     // places of the run from here on
+  FA_DEV bool more() const { return left > cost; }
+  FA_DEV int n() const { return nt - t0 < left - cost ? nt - t0 : static_cast<int>(left - cost); }
   FA_DEV void next(const CacheView& c, int hms) {
-    left -= n();
+    left -= cost + n();
     t0 = 0;
+    cost = kUnitCost;
     if (++hm == hms) {
       hm = 0;
       ++b;
-      if (left > 0) nt = tiles_of(c, b);
+      if (more()) nt = tiles_of(c, b);
     }
   }
 };
@@ -215,47 +221,41 @@ FA_DEV uint32_t swz_row(int row) {
   return SWB == 128 ? row & 7 : (row >> 1) & 3;
 }
 
-// Value rows of a tile that is not all prefix, looked after by the four softmax warps (one
-// row per thread, which have all met): rows behind the end become zero, as 0 * NaN would
-// reach every row of the product; infinities and NaNs of drafted tokens are taken out and
-// noted in the poison of the rows that see the token.  Loops stay loops: the code runs once
-// or twice per unit.
+// Value rows of a tile that is not all prefix, looked after by the four softmax warps
+// (which have all met): rows [last, 128), behind the end, become zero, as 0 * NaN would
+// reach every row of the product; infinities and NaNs of the drafted tokens, rows
+// [first, last), are taken out and noted in the poison of the rows that see the token.
+// bad_rows is zero before and after.
 template <int D, bool FP8, int NS>
-FA_DEV void clean_values(uint32_t tile, int row, int key, int inside, int len, bool look, int group,
-                         const uint32_t* seen, Poison<D>& poison, volatile uint32_t* bad_rows,
-                         volatile uint32_t* bad_stage) {
+FA_DEV void clean_values(uint32_t tile, int row, int first, int last, bool look, int group, const uint32_t* seen,
+                         Poison<D>& poison, uint32_t* bad_rows, volatile uint32_t* bad_stage) {
   using C = TCfg<D, FP8, NS>;
-  constexpr int GR = 128 / NS;
+  constexpr int GR = 128 / NS, U = D / 8;  // 16-byte units of a row
   constexpr uint32_t EXP = FP8 ? 0x7c00u : 0x7f80u, MANT = FP8 ? 0x03ffu : 0x007fu;
-  const int lane = row & 31;
-  auto unit = [&](int u) {
-    return tile + (u * 8 / C::CE) * (128 * C::SWB) + row * C::SWB + (((u % (C::CE / 8)) ^ swz_row<C::SWB>(row)) << 4);
+  auto unit = [&](int r, int u) {
+    return tile + (u * 8 / C::CE) * (128 * C::SWB) + r * C::SWB + (((u % (C::CE / 8)) ^ swz_row<C::SWB>(r)) << 4);
   };
-  bool bad = false;
-  if (key >= len) {
 #pragma unroll 1
-    for (int u = 0; u < D / 8; ++u) st_shared_v4(unit(u), make_uint4(0u, 0u, 0u, 0u));
-  } else if (key >= inside && look) {
+  for (int i = row; i < (128 - last) * U; i += 128) st_shared_v4(unit(last + i / U, i % U), make_uint4(0u, 0u, 0u, 0u));
+  if (look) {
 #pragma unroll 1
-    for (int u = 0; u < D / 8; ++u) {
-      const uint4 v = ld_shared_v4(unit(u));
+    for (int i = row; i < (last - first) * U; i += 128) {
+      const int r = first + i / U;
+      const uint4 v = ld_shared_v4(unit(r, i % U));
       const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+      bool bad = false;
 #pragma unroll
       for (int e = 0; e < 4; ++e) bad |= (x[e] & EXP) == EXP || (x[e] & EXP << 16) == EXP << 16;
+      if (bad) atomicOr(bad_rows + (r >> 5), 1u << (r & 31));
     }
   }
-  const uint32_t badw = __ballot_sync(0xffffffffu, bad);
-  if (lane == 0) bad_rows[row >> 5] = badw;
-  if (key >= inside) fence_proxy_async_smem();  // the product reads what was written here
+  fence_proxy_async_smem();  // the product reads what was written here
   named_bar_sync(1, 128);
+  volatile uint32_t* words = bad_rows;
+  if ((words[0] | words[1] | words[2] | words[3]) == 0) return;
 #pragma unroll 1
   for (int i = 0; i < 128; ++i) {
-    const uint32_t word = bad_rows[i >> 5];
-    if (word == 0) {
-      i |= 31;
-      continue;
-    }
-    if (!((word >> (i & 31)) & 1u)) continue;
+    if (!((words[i >> 5] >> (i & 31)) & 1u)) continue;
     // row i's infinities and NaNs: out of the tile, into bad_stage, to the rows that see it
     if (row == i) {
 #pragma unroll 1
@@ -263,7 +263,7 @@ FA_DEV void clean_values(uint32_t tile, int row, int key, int inside, int len, b
         uint32_t pos = 0, neg = 0;
 #pragma unroll 1
         for (int u = 4 * k; u < 4 * k + 4; ++u) {
-          const uint4 v = ld_shared_v4(unit(u));
+          const uint4 v = ld_shared_v4(unit(row, u));
           uint32_t x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
@@ -276,7 +276,7 @@ FA_DEV void clean_values(uint32_t tile, int row, int key, int inside, int len, b
               x[e / 2] &= ~(0xffffu << (16 * (e & 1)));
             }
           }
-          st_shared_v4(unit(u), make_uint4(x[0], x[1], x[2], x[3]));
+          st_shared_v4(unit(row, u), make_uint4(x[0], x[1], x[2], x[3]));
         }
         bad_stage[k] = pos;
         bad_stage[4 + k] = neg;
@@ -298,13 +298,13 @@ FA_DEV void clean_values(uint32_t tile, int row, int key, int inside, int len, b
     }
     named_bar_sync(1, 128);
   }
-  named_bar_sync(1, 128);  // bad_rows may be written again
+  if (row < 4) words[row] = 0u;
 }
 
 template <int D, bool FP8, int NS>
 __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
-    tree_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                const __grid_constant__ CUtensorMap tmV, const __grid_constant__ TreeArgs p) {
+    tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                const __grid_constant__ TreeArgs p) {
   using C = TCfg<D, FP8, NS>;
   constexpr int GR = 128 / NS;  // rows of a group, and keys each group weighs
   extern __shared__ uint8_t smem_raw[];
@@ -313,8 +313,8 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
   auto bar = [&](int i) -> uint32_t { return sb + C::OFF_BAR + 8 * i; };
   uint32_t* misc = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
-  volatile int* start = reinterpret_cast<volatile int*>(misc + 2);  // b, hm, t0 of the CTA's first tile
-  volatile uint32_t* bad_rows = misc + 8;                           // 4 words
+  volatile int* start = reinterpret_cast<volatile int*>(misc + 2);  // b, hm and place in the unit, of the run's first place
+  uint32_t* bad_rows = misc + 8;                                    // 4 words
   volatile uint32_t* bad_stage = misc + 12;                         // 8 words
   long long* scratch = reinterpret_cast<long long*>(smem + C::OFF_ROWS);
   const Guard guard{p.status, abort_flag};
@@ -326,24 +326,25 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
   if (threadIdx.x < C::NBAR) {
     const int i = threadIdx.x;
     // one arrival for loads and commits, one for each of four warps elsewhere
-    const bool four = i == C::B_QFREE || i == C::B_QREADY || i == C::B_OFREE || i == C::B_MEET ||
+    const bool four = i == C::B_QREADY || i == C::B_OFREE || i == C::B_MEET ||
                       (i >= C::B_SFREE && i < C::B_PFREE) || (FP8 && i >= C::B_FULL && i < C::B_EMPTY) ||
                       (i >= C::B_REMPTY && i < C::B_SFULL);
     mbar_init(bar(i), four ? 4 : 1);
     fence_mbar_init();
   }
+  if (threadIdx.x < 4) bad_rows[threadIdx.x] = 0u;
   if (warp == 1) {
     tmem_alloc(smem_u32(misc), C::TM_COLS);
     tmem_relinquish();
   }
   pdl_wait();  // everything from here on may be an earlier kernel's output
   if (threadIdx.x == 64) *abort_flag = (*reinterpret_cast<volatile int*>(p.status) != 0);
-  // this CTA's run of tiles
+  // this CTA's run
   long long lo, mine, run;
   {
     const int per = (p.B + C::NTHREADS - 1) / C::NTHREADS, b0 = threadIdx.x * per, b1 = min(b0 + per, p.B);
     long long sum = 0, total = 0;
-    for (int b = b0; b < b1; ++b) sum += tiles_of(c, b);
+    for (int b = b0; b < b1; ++b) sum += tiles_of(c, b) + kUnitCost;
     const long long before = block_prefix<C::NTHREADS>(sum, scratch, &total);
     total *= hms;
     run = quotient(total + gridDim.x - 1, gridDim.x);
@@ -353,101 +354,102 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
       long long at = before * hms;
       int b = b0;
       for (;; ++b) {
-        const long long n = static_cast<long long>(tiles_of(c, b)) * hms;
+        const long long n = static_cast<long long>(tiles_of(c, b) + kUnitCost) * hms;
         if (lo < at + n) break;
         at += n;
       }
-      const int nt = tiles_of(c, b);
+      const int places = tiles_of(c, b) + kUnitCost;
+      const int hm = static_cast<int>(quotient(lo - at, places));
       start[0] = b;
-      const int hm = static_cast<int>(quotient(lo - at, nt));
       start[1] = hm;
-      start[2] = static_cast<int>(lo - at - static_cast<long long>(hm) * nt);
+      start[2] = static_cast<int>(lo - at - static_cast<long long>(hm) * places);
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = misc[0];
-  const bool skip = *abort_flag != 0 || mine <= 0;
-  Walk w{0, 0, 0, 0, 0};
-  if (!skip) {
-    w.b = start[0], w.hm = start[1], w.t0 = start[2];
+  Walk w{0, 0, 0, 0, 0, 0};
+  if (mine > 0) {
+    w.b = start[0], w.hm = start[1];
+    w.t0 = max(start[2] - kUnitCost, 0), w.cost = max(kUnitCost - start[2], 0);
     w.nt = tiles_of(c, w.b);
     w.left = mine;
   }
+  const bool skip = *abort_flag != 0 || !w.more();
 
   if (warp < 4) {
     if constexpr (FP8) regs_dec<80>();
-    if (warp == 0 && !skip) {
-      // ---------------------------------------------------------------- producer (the whole warp)
+    if ((warp == 0 || warp == 3) && !skip) {
+      // ---------------------------------------------------------------- producers: warp 0 K, warp 3 V
+      const int kv = warp == 0 ? 0 : 1;
       const int rb = c.page < kKeys ? c.page : kKeys;  // rows of a box: a page, or a tile's share of one
       const int boxes = kKeys / rb;
       const int nowhere = c.pages * c.Hk;              // past the end: TMA fills zeros
-      const int pi = FP8 ? lane : lane / C::NCH, ch = FP8 ? 0 : lane % C::NCH;
-      const bool issues = pi < boxes;
+      const CUtensorMap* map = kv ? &tmV : &tmK;
+      const bool issues = lane < boxes;                // lane i looks up box i
       bool ok = true;
-      int items = 0, seg = 0, slot = 0;
-      uint32_t parity = 1;  // (a fresh barrier's phase of parity 1 counts as complete: the first trips do not wait)
       constexpr int NR = FP8 ? C::NRAW : C::NSLOT, BFULL = FP8 ? C::B_RFULL : C::B_FULL,
                     BEMPTY = FP8 ? C::B_REMPTY : C::B_EMPTY;
-      for (; ok && w.more(); ++seg) {
-        const int len = seq_len(c, w.b), h = p.M == 1 ? w.hm : w.hm / p.M, mt = w.hm - h * p.M;
-        const int n = w.n();
-        auto entry = [&](int tile) { return table_entry(c, w.b, tile * kKeys + pi * rb); };
+      int items = 0, slot = kv;
+      uint32_t parity = 1;  // (a fresh barrier's phase of parity 1 counts as complete: the first trips do not wait)
+      while (ok && w.more()) {
+        auto entry = [&](int tile) { return table_entry(c, w.b, tile * kKeys + (issues ? lane : 0) * rb); };
         int next = entry(w.t0);  // loaded a tile ahead, looked at when used
-        // the softmax warps have taken the Q before it
-        if (seg > 0 && !(ok = mbar_wait_warp(bar(C::B_QFREE), (seg - 1) & 1, guard, SITE_TREE_PRODUCER))) break;
-        if (lane == 0) {
-          mbar_expect_tx(bar(C::B_Q), GR * D * 2);
-          for (int k = 0; k < C::NCH; ++k)
-            tma_load_3d(sb + C::OFF_Q + k * GR * C::SWB, &tmQ, bar(C::B_Q), k * C::CE, mt * 128, w.b * c.Hk + h);
-        }
-        for (int j = 0; ok && j < n; ++j) {
+        const int len = seq_len(c, w.b), h = p.M == 1 ? w.hm : w.hm / p.M;
+        const int n = w.n();
+        for (int j = 0; j < n; ++j) {
           const int tile = w.t0 + j;
-          const int y = (tile * kKeys + pi * rb) & (c.page - 1);
           // this lane's box: z coordinate of its page and head
-          const int z = issues && tile * kKeys + pi * rb < len && next >= 0 && next < c.pages ? next * c.Hk + h : nowhere;
+          const int z = issues && tile * kKeys + lane * rb < len && next >= 0 && next < c.pages ? next * c.Hk + h : nowhere;
           if (j + 1 < n) next = entry(tile + 1);
-          for (int kv = 0; kv < 2; ++kv) {
-            if (!(ok = mbar_wait_warp(bar(BEMPTY + slot), parity, guard, SITE_TREE_PRODUCER))) break;
-            const uint32_t full = bar(BFULL + slot);
-            if constexpr (FP8) {
-              const uint32_t dst = sb + C::OFF_RAW + slot * C::RAW, exps = dst + 128 * D + pi * rb;
-              const bool there = issues && z != nowhere;
-              const int n_there = __popc(__ballot_sync(0xffffffffu, there));
-              if (kv == 0 && issues && !there) {  // no page, no exponents: 2^-127
-                for (int k = 0; k < rb; k += 16) {
-                  st_shared_v4(exps + k, make_uint4(0u, 0u, 0u, 0u));
-                  st_shared_v4(exps + 128 + k, make_uint4(0u, 0u, 0u, 0u));
-                }
-                fence_proxy_async_smem();
+          const int y = (tile * kKeys) & (c.page - 1);  // a tile's place in a page of more than a tile
+          if (!(ok = mbar_wait_warp(bar(BEMPTY + slot), parity, guard, SITE_TREE_PRODUCER))) break;
+          const uint32_t full = bar(BFULL + slot);
+          if constexpr (FP8) {
+            const uint32_t dst = sb + C::OFF_RAW + slot * C::RAW, exps = dst + 128 * D + lane * rb;
+            const bool there = issues && z != nowhere;
+            const int n_there = __popc(__ballot_sync(0xffffffffu, there));
+            if (kv == 0 && issues && !there) {  // no page, no exponents: 2^-127
+              for (int k = 0; k < rb; k += 16) {
+                st_shared_v4(exps + k, make_uint4(0u, 0u, 0u, 0u));
+                st_shared_v4(exps + 128 + k, make_uint4(0u, 0u, 0u, 0u));
               }
-              __syncwarp();
-              if (lane == 0) mbar_expect_tx(full, 128 * D + (kv == 0 ? 2 * n_there * rb : 0));
-              __syncwarp();
-              if (issues) tma_load_3d(dst + pi * rb * D, kv ? &tmV : &tmK, full, 0, y, z);
-              if (kv == 0 && there) {
-                bulk_load(exps, c.Ke + static_cast<size_t>(z) * c.page + y, rb, full);
-                bulk_load(exps + 128, c.Ve + static_cast<size_t>(z) * c.page + y, rb, full);
-              }
-            } else {
-              if (lane == 0) mbar_expect_tx(full, C::TILE);
-              __syncwarp();
-              if (issues)
-                tma_load_3d(sb + C::OFF_T + slot * C::TILE + ch * 128 * C::SWB + pi * rb * C::SWB, kv ? &tmV : &tmK, full,
-                            ch * C::CE, y, z);
+              fence_proxy_async_smem();
             }
-            ++items;
-            if (++slot == NR) slot = 0, parity ^= 1;
+            __syncwarp();
+            if (lane == 0) mbar_expect_tx(full, 128 * D + (kv == 0 ? 2 * n_there * rb : 0));
+            for (int i = 0; i < boxes; ++i) {
+              const int zi = __shfl_sync(0xffffffffu, z, i);
+              if (lane == 0) {
+                tma_load_3d(dst + i * rb * D, map, full, 0, y, zi);
+                if (kv == 0 && zi != nowhere) {
+                  const size_t at = static_cast<size_t>(zi) * c.page + y;
+                  bulk_load(dst + 128 * D + i * rb, c.Ke + at, rb, full);
+                  bulk_load(dst + 128 * D + 128 + i * rb, c.Ve + at, rb, full);
+                }
+              }
+            }
+          } else {
+            if (lane == 0) mbar_expect_tx(full, C::TILE);
+            for (int i = 0; i < boxes; ++i) {
+              const int zi = __shfl_sync(0xffffffffu, z, i);
+              if (lane == 0)
+                for (int ch = 0; ch < D / C::CE; ++ch)
+                  tma_load_3d(sb + C::OFF_T + slot * C::TILE + ch * 128 * C::SWB + i * rb * C::SWB, map, full, ch * C::CE, y,
+                              zi);
+            }
           }
+          ++items;
+          if ((slot += 2) >= NR) slot -= NR, parity ^= 1;
         }
+        if (!ok) break;
         w.next(c, hms);
       }
       if (*abort_flag && lane == 0) {
         // gave up: let every load this warp started land before the CTA exits
-        if (seg > 0) mbar_drain(bar(C::B_Q), (seg - 1) & 1);
-        mbar_drain(bar(C::B_Q), seg & 1);
-        for (int i = items > NR ? items - NR : 0; i < items; ++i) mbar_drain(bar(BFULL + i % NR), (i / NR) & 1);
+        for (int i = items > NR / 2 ? items - NR / 2 : 0; i < items; ++i)
+          mbar_drain(bar(BFULL + (2 * i + kv) % NR), ((2 * i + kv) / NR) & 1);
       }
     } else if (warp == 1 && lane == 0 && !skip) {
       // ---------------------------------------------------------------- UMMA issuer: S = Q (tensor memory) x K
@@ -532,23 +534,24 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
         meet_parity ^= 1;
         return __all_sync(0xffffffffu, all);
       };
-      // This thread's row of the next unit's Q into tensor memory; returns what a score is multiplied by.
+      // This thread's row of a unit's Q into tensor memory; q_scale: what its scores are multiplied by.
       // For an e4m3 cache the row becomes f16, scaled by a power of two to a maximum in [2^14, 2^15): elements
       // of 2^-31 of the maximum and more keep all their bits.
       float q_scale = 0.f;
-      auto take_q = [&](int s) -> bool {
-        if (!mbar_wait_warp(bar(C::B_Q), s & 1, guard, SITE_TREE_SOFTMAX)) return false;
-        const uint32_t qrow = sb + C::OFF_Q + r_in * C::SWB;
-        auto unit = [&](int u) {  // 8 elements
-          return ld_shared_v4(qrow + (u / (C::CE / 8)) * (GR * C::SWB) + (((u % (C::CE / 8)) ^ swz_row<C::SWB>(r_in)) << 4));
-        };
+      auto take_q = [&](const Walk& at) {
+        const int h = p.M == 1 ? at.hm : at.hm / p.M, q = (at.hm - h * p.M) * 128 + r_in;
+        uint4 x[D / 8];
+        const uint4* src =
+            reinterpret_cast<const uint4*>(p.Q + ((static_cast<size_t>(at.b) * c.Hk + h) * p.R + (q < p.R ? q : 0)) * D);
+#pragma unroll
+        for (int u = 0; u < D / 8; ++u) x[u] = src[u];  // (rows that are not there: any row, never stored)
         float mul = 1.f;
         q_scale = p.c_log2;
         if constexpr (FP8) {
           uint32_t m = 0;
 #pragma unroll
           for (int u = 0; u < D / 8; ++u) {
-            const uint4 v = unit(u);
+            const uint4 v = x[u];
             const uint32_t k = 0x7fff7fffu;
             m = __vmaxu2(m, __vmaxu2(__vmaxu2(v.x & k, v.y & k), __vmaxu2(v.z & k, v.w & k)));
           }
@@ -562,24 +565,19 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
           uint32_t o[16];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const uint4 v = unit(4 * k + i);
-            const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+            const uint32_t v[4] = {x[4 * k + i].x, x[4 * k + i].y, x[4 * k + i].z, x[4 * k + i].w};
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              o[4 * i + e] = FP8 ? pack_f16x2(__uint_as_float(x[e] << 16) * mul,
-                                              __uint_as_float(x[e] & 0xffff0000u) * mul)
-                                 : x[e];
+              o[4 * i + e] = FP8 ? pack_f16x2(__uint_as_float(v[e] << 16) * mul,
+                                              __uint_as_float(v[e] & 0xffff0000u) * mul)
+                                 : v[e];
           }
           tmem_st16(tl + C::TM_Q + 16 * k, o);
         }
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(bar(C::B_QFREE));
-          mbar_arrive(bar(C::B_QREADY));
-        }
-        return true;
+        if (lane == 0) mbar_arrive(bar(C::B_QREADY));
       };
       // The other groups' weights are zero, for good: a tile writes its own group's columns only.
       if constexpr (NS > 1) {
@@ -589,7 +587,7 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
 #pragma unroll
         for (int k = 0; k < C::NPB * 4; ++k) tmem_st16(tl + C::TM_P0 + 16 * k, zero);
       }
-      ok = take_q(0);
+      take_q(w);
       // What a unit starts with is loaded before the epilogue of the one before it
       // (as it is in memory, so that the loads are all under way at once).
       auto new_of = [&](int i) { return c.n_new == nullptr ? c.T : c.n_new[i]; };
@@ -763,8 +761,10 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
           }
           if (k0 + kKeys > inside) {  // the tile holds drafted tokens or rows behind the end
             if (!(ok = mbar_wait_warp(bar(C::B_FULL + vs_slot), vpar, guard, SITE_TREE_SOFTMAX)) || !(ok = meet())) break;
-            clean_values<D, FP8, NS>(sb + C::OFF_T + vs_slot * C::TILE, row, k0 + row, inside, len,
-                                     c.T > 1 || p.tree != nullptr, group, seen, poison, bad_rows, bad_stage);
+            // (a single token sees itself, or its row sees nothing at all: its values need no look)
+            clean_values<D, FP8, NS>(sb + C::OFF_T + vs_slot * C::TILE, row, max(inside - k0, 0),
+                                     min(max(len - k0, 0), 128), c.T > 1 || p.tree != nullptr, group, seen, poison,
+                                     bad_rows, bad_stage);
           }
           tc_fence_before();
           __syncwarp();
@@ -780,13 +780,13 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
         w.next(c, hms);
         if (w.more()) {
           raw_len = c.lens[w.b], raw_new = new_of(w.b), entry = page_entry(w.t0);
-          if (!(ok = take_q(seg + 1))) break;  // the next unit's S may be formed meanwhile
+          take_q(w);  // the next unit's S may be formed meanwhile
         }
         if (!(ok = mbar_wait_warp(bar(C::B_OFULL), seg & 1, guard, SITE_TREE_SOFTMAX)) || !(ok = meet())) break;
         tc_fence_after();
         const bool whole = at.t0 == 0 && n == at.nt;
         if (at.t0 == 0 && tid == 0) {
-          const long long first = lo + mine - at.left;  // the unit's first tile among all tiles
+          const long long first = lo + mine - at.left + at.cost;  // the place of the unit's first tile
           p.info[static_cast<long long>(at.b) * hms + at.hm] =
               UnitInfo{static_cast<int>(blockIdx.x), static_cast<int>(quotient(first + at.nt - 1, run))};
         }
@@ -846,7 +846,7 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
           // The groups' rows are added up through shared memory, XR rows at a time: every thread then has EPT
           // elements of one of them.
           constexpr int XR = 16384 / (NS * D * 4), TPR = 128 / XR, EPT = D / TPR;
-          static_assert(EPT == 8 * (4 / NS) || EPT >= 8, "whole 16-byte pieces");
+          static_assert(EPT % 8 == 0, "whole 16-byte pieces of O");
           rows[row] = ref;
           rows[128 + row] = l;
           rows[256 + row] = lr;
@@ -901,27 +901,29 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
 #pragma unroll
               for (int k = 0; k < EPT / 4; ++k) {
                 float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                const int piece = (k / 2 * TPR + part) * 2 + (k & 1);  // eight elements here, eight TPR * 8 on
 #pragma unroll
                 for (int g = 0; g < NS; ++g) {
-                  const float4 y = xch[(g * XR + tid / TPR) * (D / 4) + ((part * (EPT / 4) + k) ^ ((tid / TPR) & 7))];
+                  const float4 y = xch[(g * XR + tid / TPR) * (D / 4) + (piece ^ ((tid / TPR) & 7))];
                   v.x += y.x, v.y += y.y, v.z += y.z, v.w += y.w;
                 }
                 a[4 * k] = v.x, a[4 * k + 1] = v.y, a[4 * k + 2] = v.z, a[4 * k + 3] = v.w;
               }
               const float inv = olr == 0.f ? 0.f : 1.f / olr;
               if (whole) {
-                uint4* dst = reinterpret_cast<uint4*>(p.O + (row0 + orow) * D + part * EPT);
+                uint4* dst = reinterpret_cast<uint4*>(p.O + (row0 + orow) * D) + part;
 #pragma unroll
                 for (int k = 0; k < EPT / 8; ++k)
-                  dst[k] = make_uint4(pack_bf16x2(a[8 * k] * inv, a[8 * k + 1] * inv),
+                  dst[k * TPR] = make_uint4(pack_bf16x2(a[8 * k] * inv, a[8 * k + 1] * inv),
                                       pack_bf16x2(a[8 * k + 2] * inv, a[8 * k + 3] * inv),
                                       pack_bf16x2(a[8 * k + 4] * inv, a[8 * k + 5] * inv),
                                       pack_bf16x2(a[8 * k + 6] * inv, a[8 * k + 7] * inv));
                 if (part == 0) p.L[row0 + orow] = olr == 0.f ? -INFINITY : (om + lg2(ol)) * kFwdLn2;
               } else {
-                float4* dst = reinterpret_cast<float4*>(slot + static_cast<size_t>(orow) * D + part * EPT);
+                float4* dst = reinterpret_cast<float4*>(slot + static_cast<size_t>(orow) * D) + 2 * part;
 #pragma unroll
-                for (int k = 0; k < EPT / 4; ++k) dst[k] = make_float4(a[4 * k], a[4 * k + 1], a[4 * k + 2], a[4 * k + 3]);
+                for (int k = 0; k < EPT / 4; ++k)
+                  dst[k / 2 * TPR * 2 + (k & 1)] = make_float4(a[4 * k], a[4 * k + 1], a[4 * k + 2], a[4 * k + 3]);
                 if (part == 0) sums[orow] = om, sums[p.rows + orow] = ol, sums[2 * p.rows + orow] = olr;
               }
             }
@@ -951,7 +953,7 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
       bool ok = true;
       int rs = kv % C::NRAW, s = kv, sc = 0;  // slots of the rings
       uint32_t rpar = 0, spar = 1;
-      for (long long left = mine; ok && left > 0; --left) {
+      for (int left = w.n(); ok && left > 0;) {
         if (!(ok = mbar_wait_warp(bar(C::B_RFULL + rs), rpar, guard, SITE_TREE_CONVERT))) break;
         const uint32_t raw = sb + C::OFF_RAW + rs * C::RAW, dst = sb + C::OFF_T + s * C::TILE;
         uint4 x[NP];
@@ -993,6 +995,10 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
         if (lane == 0) mbar_arrive(bar(C::B_FULL + s));
         if ((rs += 2) >= C::NRAW) rs -= C::NRAW, rpar ^= 1;
         if ((s += 2) >= C::NSLOT) s -= C::NSLOT, spar ^= 1;
+        if (--left == 0) {
+          w.next(c, hms);
+          left = w.more() ? w.n() : 0;
+        }
       }
     }
   }
@@ -1096,12 +1102,11 @@ int slot_rows(int R) { return R <= 32 ? 32 : R <= 64 ? 64 : 128; }
 size_t info_bytes(long long units) { return (static_cast<size_t>(units) * sizeof(UnitInfo) + 255) / 256 * 256; }
 
 template <int D, bool FP8, int NS>
-fa_status launch_tree(const TreeArgs& p, const void* Q, int grid, cudaStream_t stream) {
+fa_status launch_tree(const TreeArgs& p, int grid, cudaStream_t stream) {
   using C = TCfg<D, FP8, NS>;
   const CacheView& c = p.c;
-  CUtensorMap mQ, mK, mV;
+  CUtensorMap mK, mV;
   const int rb = c.page < kKeys ? c.page : kKeys, heads = c.pages * c.Hk;
-  if (!encode_bf16_3d(&mQ, Q, D, p.R, p.B * c.Hk, C::CE, 128 / NS)) return FA_ERR_CUDA;
   if (FP8) {
     if (!encode_u8_3d(&mK, c.K, D, c.page, heads, D, rb) || !encode_u8_3d(&mV, c.V, D, c.page, heads, D, rb))
       return FA_ERR_CUDA;
@@ -1112,7 +1117,7 @@ fa_status launch_tree(const TreeArgs& p, const void* Q, int grid, cudaStream_t s
   auto kern = tree_kernel<D, FP8, NS>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
     return FA_ERR_CUDA;
-  if (launch_pdl(kern, dim3(grid), dim3(C::NTHREADS), C::SMEM, stream, mQ, mK, mV, p) != cudaSuccess)
+  if (launch_pdl(kern, dim3(grid), dim3(C::NTHREADS), C::SMEM, stream, mK, mV, p) != cudaSuccess)
     return FA_ERR_CUDA;
   const unsigned units = static_cast<unsigned>(p.B) * c.Hk * p.M;
   const int n = p.R < 128 ? p.R : 128;
@@ -1121,10 +1126,10 @@ fa_status launch_tree(const TreeArgs& p, const void* Q, int grid, cudaStream_t s
 }
 
 template <int D, bool FP8>
-fa_status launch_tree_rows(const TreeArgs& p, const void* Q, int grid, cudaStream_t s) {
-  return p.R <= 32   ? launch_tree<D, FP8, 4>(p, Q, grid, s)
-         : p.R <= 64 ? launch_tree<D, FP8, 2>(p, Q, grid, s)
-                     : launch_tree<D, FP8, 1>(p, Q, grid, s);
+fa_status launch_tree_rows(const TreeArgs& p, int grid, cudaStream_t s) {
+  return p.R <= 32   ? launch_tree<D, FP8, 4>(p, grid, s)
+         : p.R <= 64 ? launch_tree<D, FP8, 2>(p, grid, s)
+                     : launch_tree<D, FP8, 1>(p, grid, s);
 }
 
 }  // namespace
@@ -1164,6 +1169,7 @@ fa_status fa_fwd_tree(const void* Q, const fa_cache* cache, void* O, float* L, i
   if (workspace == nullptr || workspace_bytes < need || !aligned(workspace, 16)) return FA_ERR_WORKSPACE;
   p.status = device_status_word();
   if (p.status == nullptr) return FA_ERR_CUDA;
+  p.Q = static_cast<const __nv_bfloat16*>(Q);
   p.O = static_cast<__nv_bfloat16*>(O);
   p.L = L;
   p.tree = tree;
@@ -1190,10 +1196,10 @@ fa_status fa_fwd_tree(const void* Q, const fa_cache* cache, void* O, float* L, i
   if (most < grid) grid = static_cast<int>(most);
   const bool fp8 = cache->format == FA_CACHE_E4M3;
   switch (cache->d) {
-    case 32: return fp8 ? launch_tree_rows<32, true>(p, Q, grid, stream) : launch_tree_rows<32, false>(p, Q, grid, stream);
-    case 64: return fp8 ? launch_tree_rows<64, true>(p, Q, grid, stream) : launch_tree_rows<64, false>(p, Q, grid, stream);
+    case 32: return fp8 ? launch_tree_rows<32, true>(p, grid, stream) : launch_tree_rows<32, false>(p, grid, stream);
+    case 64: return fp8 ? launch_tree_rows<64, true>(p, grid, stream) : launch_tree_rows<64, false>(p, grid, stream);
     default:
-      return fp8 ? launch_tree_rows<128, true>(p, Q, grid, stream) : launch_tree_rows<128, false>(p, Q, grid, stream);
+      return fp8 ? launch_tree_rows<128, true>(p, grid, stream) : launch_tree_rows<128, false>(p, grid, stream);
   }
 }
 
