@@ -40,7 +40,6 @@
 // NaN value of a drafted token is taken out of the product too and goes only to the
 // rows that see the token (`Poison`).
 #include <cuda_fp16.h>
-#include <cuda_fp8.h>
 
 #include <cmath>
 
@@ -193,10 +192,11 @@ struct Poison {
   uint32_t pos[D / 32], neg[D / 32];
 };
 
-// Two e4m3 numbers as two f16 numbers, exactly.
-FA_DEV uint32_t e4m3x2_to_f16x2(uint32_t two) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two), __NV_E4M3);
-  return static_cast<uint32_t>(h.x) | static_cast<uint32_t>(h.y) << 16;
+// Four e4m3 numbers as four f16 numbers, exactly.
+FA_DEV void e4m3x4_to_f16x4(uint32_t four, uint32_t& lo, uint32_t& hi) {
+  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.rn.f16x2.e4m3x2 %0, l;\n cvt.rn.f16x2.e4m3x2 %1, h;\n}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(four));
 }
 FA_DEV uint32_t pack_f16x2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
@@ -404,7 +404,7 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
           const int z = issues && tile * kKeys + lane * rb < len && next >= 0 && next < c.pages ? next * c.Hk + h : nowhere;
           if (j + 1 < n) next = entry(tile + 1);
           const int y = (tile * kKeys) & (c.page - 1);  // a tile's place in a page of more than a tile
-          if (!(ok = mbar_wait_warp(bar(BEMPTY + slot), parity, guard, SITE_TREE_PRODUCER))) break;
+          if (!(ok = mbar_rest_warp(bar(BEMPTY + slot), parity, guard, SITE_TREE_PRODUCER))) break;
           const uint32_t full = bar(BFULL + slot);
           if constexpr (FP8) {
             const uint32_t dst = sb + C::OFF_RAW + slot * C::RAW, exps = dst + 128 * D + lane * rb;
@@ -459,11 +459,11 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
       uint32_t bpar = 1, spar = 0;
       for (; ok && w.more(); ++seg) {
         const int n = w.n();
-        if (!(ok = mbar_wait(bar(C::B_QREADY), seg & 1, guard, SITE_TREE_MMA))) break;
+        if (!(ok = mbar_rest(bar(C::B_QREADY), seg & 1, guard, SITE_TREE_MMA))) break;
         for (int j = 0; j < n; ++j) {
           // the scores that were in S buffer b have been read
-          if (!(ok = mbar_wait(bar(C::B_SFREE + b), bpar, guard, SITE_TREE_MMA))) break;
-          if (!(ok = mbar_wait(bar(C::B_FULL + s), spar, guard, SITE_TREE_MMA))) break;
+          if (!(ok = mbar_rest(bar(C::B_SFREE + b), bpar, guard, SITE_TREE_MMA))) break;
+          if (!(ok = mbar_rest(bar(C::B_FULL + s), spar, guard, SITE_TREE_MMA))) break;
           tc_fence_after();
           const uint32_t kb = sb + C::OFF_T + s * C::TILE;
 #pragma unroll
@@ -487,10 +487,10 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
       for (; ok && w.more(); ++seg) {
         const int n = w.n();
         for (int j = 0; j < n; ++j) {
-          if (!(ok = mbar_wait(bar(C::B_PFULL + b), bpar, guard, SITE_TREE_MMA))) break;
-          if (!(ok = mbar_wait(bar(C::B_FULL + s), spar, guard, SITE_TREE_MMA))) break;
+          if (!(ok = mbar_rest(bar(C::B_PFULL + b), bpar, guard, SITE_TREE_MMA))) break;
+          if (!(ok = mbar_rest(bar(C::B_FULL + s), spar, guard, SITE_TREE_MMA))) break;
           // a unit's first product overwrites O: the epilogue before it has read it
-          if (j == 0 && seg > 0 && !(ok = mbar_wait(bar(C::B_OFREE), (seg - 1) & 1, guard, SITE_TREE_MMA))) break;
+          if (j == 0 && seg > 0 && !(ok = mbar_rest(bar(C::B_OFREE), (seg - 1) & 1, guard, SITE_TREE_MMA))) break;
           tc_fence_after();
           const uint32_t vb = sb + C::OFF_T + s * C::TILE, aP = tmem + C::TM_P0 + b * 64;
 #pragma unroll
@@ -529,7 +529,7 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
         if (lane == 0) mbar_arrive(bar(C::B_MEET));
         const uint64_t t0 = gtimer_ns();
         bool all;
-        while (!(all = mbar_try(bar(C::B_MEET), meet_parity)) && gtimer_ns() - t0 <= 2 * kWaitLimitNs) {
+        while (!(all = mbar_try_rest(bar(C::B_MEET), meet_parity)) && gtimer_ns() - t0 <= 2 * kWaitLimitNs) {
         }
         meet_parity ^= 1;
         return __all_sync(0xffffffffu, all);
@@ -632,7 +632,7 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
               seen[i] = live ? m & in_page : 0u;
             }
           }
-          if (!(ok = mbar_wait_warp(bar(C::B_SFULL + b), bpar, guard, SITE_TREE_SOFTMAX))) break;
+          if (!(ok = mbar_rest_warp(bar(C::B_SFULL + b), bpar, guard, SITE_TREE_SOFTMAX))) break;
           tc_fence_after();
           if (warp_live) {
             uint32_t r[GR];
@@ -693,7 +693,7 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
                 if (move) l *= alpha, lr *= alpha, ref = new_ref;
                 // the product that last wrote O is done
                 const int last = pb == 0 ? C::NPB - 1 : pb - 1;
-                if (!(ok = mbar_wait_warp(bar(C::B_PFREE + last), C::NPB == 1 || pb != 0 ? pfree ^ (C::NPB > 1) : pfree, guard,
+                if (!(ok = mbar_rest_warp(bar(C::B_PFREE + last), C::NPB == 1 || pb != 0 ? pfree ^ (C::NPB > 1) : pfree, guard,
                                           SITE_TREE_SOFTMAX)))
                   break;
                 tc_fence_after();
@@ -745,7 +745,7 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
             // bf16 weights are normalised by their own sum; f16 ones are off by 2^-11 at most
             lr = FP8 ? l : lr + (rl[0] + rl[1]) + (rh[0] + rh[1]);
             // the product that read this P buffer is done
-            if (!(ok = mbar_wait_warp(bar(C::B_PFREE + pb), pfree, guard, SITE_TREE_SOFTMAX))) break;
+            if (!(ok = mbar_rest_warp(bar(C::B_PFREE + pb), pfree, guard, SITE_TREE_SOFTMAX))) break;
             tc_fence_after();
             const uint32_t own = tl + C::TM_P0 + pb * 64 + group * (GR / 2);
             if constexpr (NS == 4) tmem_st16(own, pk);
@@ -760,7 +760,7 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
             if (lane == 0) mbar_arrive(bar(C::B_SFREE + b));
           }
           if (k0 + kKeys > inside) {  // the tile holds drafted tokens or rows behind the end
-            if (!(ok = mbar_wait_warp(bar(C::B_FULL + vs_slot), vpar, guard, SITE_TREE_SOFTMAX)) || !(ok = meet())) break;
+            if (!(ok = mbar_rest_warp(bar(C::B_FULL + vs_slot), vpar, guard, SITE_TREE_SOFTMAX)) || !(ok = meet())) break;
             // (a single token sees itself, or its row sees nothing at all: its values need no look)
             clean_values<D, FP8, NS>(sb + C::OFF_T + vs_slot * C::TILE, row, max(inside - k0, 0),
                                      min(max(len - k0, 0), 128), c.T > 1 || p.tree != nullptr, group, seen, poison,
@@ -782,7 +782,7 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
           raw_len = c.lens[w.b], raw_new = new_of(w.b), entry = page_entry(w.t0);
           take_q(w);  // the next unit's S may be formed meanwhile
         }
-        if (!(ok = mbar_wait_warp(bar(C::B_OFULL), seg & 1, guard, SITE_TREE_SOFTMAX)) || !(ok = meet())) break;
+        if (!(ok = mbar_rest_warp(bar(C::B_OFULL), seg & 1, guard, SITE_TREE_SOFTMAX)) || !(ok = meet())) break;
         tc_fence_after();
         const bool whole = at.t0 == 0 && n == at.nt;
         if (at.t0 == 0 && tid == 0) {
@@ -954,7 +954,7 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
       int rs = kv % C::NRAW, s = kv, sc = 0;  // slots of the rings
       uint32_t rpar = 0, spar = 1;
       for (int left = w.n(); ok && left > 0;) {
-        if (!(ok = mbar_wait_warp(bar(C::B_RFULL + rs), rpar, guard, SITE_TREE_CONVERT))) break;
+        if (!(ok = mbar_rest_warp(bar(C::B_RFULL + rs), rpar, guard, SITE_TREE_CONVERT))) break;
         const uint32_t raw = sb + C::OFF_RAW + rs * C::RAW, dst = sb + C::OFF_T + s * C::TILE;
         uint4 x[NP];
 #pragma unroll
@@ -966,7 +966,7 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(C::B_REMPTY + rs));  // the next tile may come while this one is converted
-        if (!(ok = mbar_wait_warp(bar(C::B_EMPTY + s), spar, guard, SITE_TREE_CONVERT))) break;
+        if (!(ok = mbar_rest_warp(bar(C::B_EMPTY + s), spar, guard, SITE_TREE_CONVERT))) break;
         if (kv == 0) {
           // The tile's scales, for the softmax warps.  This slot held the K tile NSLOT / 2 tiles ago, whose S is
           // done; so the P of NSB tiles before that was used, and the softmax is past it: the NSLOT / 2 + NSB - 1
@@ -983,10 +983,7 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
           const uint32_t w4[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
           uint32_t o[8];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            o[2 * q] = e4m3x2_to_f16x2(w4[q] & 0xffffu);
-            o[2 * q + 1] = e4m3x2_to_f16x2(w4[q] >> 16);
-          }
+          for (int q = 0; q < 4; ++q) e4m3x4_to_f16x4(w4[q], o[2 * q], o[2 * q + 1]);
           st_shared_v4(dst + to0 + k * ROWS * C::SWB, make_uint4(o[0], o[1], o[2], o[3]));
           st_shared_v4(dst + to1 + k * ROWS * C::SWB, make_uint4(o[4], o[5], o[6], o[7]));
         }
