@@ -48,7 +48,7 @@ FA_DEV int page_of(const CacheView& c, int b, int j) {
 }
 
 // The table's entry for row j, whatever j is (beyond the table: its last column); to be
-// compared with [0, pages) by the caller.  Needs cols > 0.
+// compared with [0, pages) by the caller.  Needs cols > 0; j up to 2^30 + 2^26.
 FA_DEV int table_entry(const CacheView& c, int b, int j) {
   return c.table[b * c.table_stride + min(j >> c.page_shift, c.cols - 1)];
 }

@@ -82,10 +82,13 @@ struct TCfg {
   static constexpr int SWB = (D * 2 >= 128) ? 128 : D * 2;
   static constexpr int CE = SWB / 2;
   static constexpr int TILE = 128 * D * 2;
-  static constexpr int NSLOT = FP8 ? (D == 128 ? 4 : 6) : (D == 128 ? 6 : 8);  // 16-bit tiles, K and V in turn
-  static constexpr int NRAW = FP8 ? (D == 128 ? 4 : 6) : 0;  // e4m3 tiles
-  // K tiles use the even slots of a ring and V tiles the odd ones, each with a producer and a consumer of its own.
-  static_assert(NSLOT % 2 == 0 && NRAW % 2 == 0, "disjoint slots");
+  static constexpr int NSLOT = D < 128 ? 8 : FP8 ? 4 : 6;  // 16-bit tiles, K and V in turn
+  static constexpr int NRAW = FP8 ? NSLOT : 0;             // e4m3 tiles
+  // K tiles use the even slots of a ring and V tiles the odd ones, and the two pairs of warps that take an e4m3
+  // cache's tiles in turn have slots of their own too (4 divides NSLOT and NRAW).  So each slot's barriers are waited
+  // for by one party that sees every phase of them: with a slot shared, a party that is a tile ahead would take the
+  // other's phase for its own.
+  static_assert(NSLOT % 2 == 0 && (!FP8 || (NSLOT % 4 == 0 && NRAW % 4 == 0)), "slots of their own");
   static constexpr int RAW = 128 * D + 256;     // with the exponent bytes of its keys (K tiles: and of their values)
   static constexpr int NSB = 2;                 // S buffers in tensor memory
   static constexpr int NPB = D == 128 ? 1 : 2;  // P buffers
@@ -142,6 +145,31 @@ struct Walk {
       ++b;
       if (more()) nt = tiles_of(c, b);
     }
+  }
+};
+
+// A warp's window on a sequence's page table, 32 entries (boxes) at a time, one per lane,
+// the next 32 under way: while the SMs stream the cache, a load takes some 2400 cycles,
+// more than a tile.
+struct TableWindow {
+  int now, next, pos, row;  // row: first of the 32 rows' boxes that `next` holds
+  FA_DEV void open(const CacheView& c, int b, int first_row, int rb, int lane) {
+    now = table_entry(c, b, first_row + lane * rb);
+    row = first_row + 32 * rb;
+    next = table_entry(c, b, row + lane * rb);
+    pos = 0;
+  }
+  // The entries of the next tile's boxes, in lanes 0 .. boxes - 1.
+  FA_DEV int take(const CacheView& c, int b, int boxes, int rb, int lane) {
+    const int e = __shfl_sync(0xffffffffu, now, (pos + lane) & 31);
+    pos += boxes;
+    if (pos == 32) {
+      pos = 0;
+      now = next;
+      row += 32 * rb;
+      next = table_entry(c, b, row + lane * rb);
+    }
+    return e;
   }
 };
 
@@ -326,10 +354,10 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
   if (threadIdx.x < C::NBAR) {
     const int i = threadIdx.x;
     // one arrival for loads and commits, one for each of four warps elsewhere
-    const bool four = i == C::B_QREADY || i == C::B_OFREE || i == C::B_MEET ||
-                      (i >= C::B_SFREE && i < C::B_PFREE) || (FP8 && i >= C::B_FULL && i < C::B_EMPTY) ||
-                      (i >= C::B_REMPTY && i < C::B_SFULL);
-    mbar_init(bar(i), four ? 4 : 1);
+    const bool four = i == C::B_QREADY || i == C::B_OFREE || i == C::B_MEET || (i >= C::B_SFREE && i < C::B_PFREE);
+    // (and of two where the e4m3 tiles are converted)
+    const bool two = FP8 && ((i >= C::B_FULL && i < C::B_EMPTY) || (i >= C::B_REMPTY && i < C::B_SFULL));
+    mbar_init(bar(i), four ? 4 : two ? 2 : 1);
     fence_mbar_init();
   }
   if (threadIdx.x < 4) bad_rows[threadIdx.x] = 0u;
@@ -394,15 +422,15 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
       int items = 0, slot = kv;
       uint32_t parity = 1;  // (a fresh barrier's phase of parity 1 counts as complete: the first trips do not wait)
       while (ok && w.more()) {
-        auto entry = [&](int tile) { return table_entry(c, w.b, tile * kKeys + (issues ? lane : 0) * rb); };
-        int next = entry(w.t0);  // loaded a tile ahead, looked at when used
+        TableWindow table;
+        table.open(c, w.b, w.t0 * kKeys, rb, lane);
         const int len = seq_len(c, w.b), h = p.M == 1 ? w.hm : w.hm / p.M;
         const int n = w.n();
         for (int j = 0; j < n; ++j) {
           const int tile = w.t0 + j;
           // this lane's box: z coordinate of its page and head
-          const int z = issues && tile * kKeys + lane * rb < len && next >= 0 && next < c.pages ? next * c.Hk + h : nowhere;
-          if (j + 1 < n) next = entry(tile + 1);
+          const int page = table.take(c, w.b, boxes, rb, lane);
+          const int z = issues && tile * kKeys + lane * rb < len && page >= 0 && page < c.pages ? page * c.Hk + h : nowhere;
           const int y = (tile * kKeys) & (c.page - 1);  // a tile's place in a page of more than a tile
           if (!(ok = mbar_rest_warp(bar(BEMPTY + slot), parity, guard, SITE_TREE_PRODUCER))) break;
           const uint32_t full = bar(BFULL + slot);
@@ -592,10 +620,8 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
       // (as it is in memory, so that the loads are all under way at once).
       auto new_of = [&](int i) { return c.n_new == nullptr ? c.T : c.n_new[i]; };
       int raw_len = c.lens[w.b], raw_new = new_of(w.b);
-      auto page_entry = [&](int tile) {  // this lane's box
-        return table_entry(c, w.b, tile * kKeys + (lane < boxes ? lane : 0) * (kKeys / boxes));
-      };
-      int entry = page_entry(w.t0);
+      TableWindow table;
+      table.open(c, w.b, w.t0 * kKeys, kKeys / boxes, lane);
       for (; ok && w.more(); ++seg) {
         const int n = w.n();
         const int h = p.M == 1 ? w.hm : w.hm / p.M, mt = w.hm - h * p.M;
@@ -614,9 +640,9 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
         for (int j = 0; j < n; ++j) {
           const int k0 = (w.t0 + j) * kKeys;
           // bit i: box i's page exists
-          const uint32_t pm = __ballot_sync(0xffffffffu, lane < boxes && k0 + lane * (kKeys / boxes) < len && entry >= 0 &&
-                                                             entry < c.pages);
-          if (j + 1 < n) entry = page_entry(w.t0 + j + 1);
+          const int page = table.take(c, w.b, boxes, kKeys / boxes, lane);
+          const uint32_t pm =
+              __ballot_sync(0xffffffffu, lane < boxes && k0 + lane * (kKeys / boxes) < len && page >= 0 && page < c.pages);
           const bool edge = k0 + kKeys > inside || pm != all_boxes;
           uint32_t seen[GR / 32];  // this row's keys of its group, 32 a word
           if (edge) {
@@ -779,7 +805,8 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
         const Walk at = w;
         w.next(c, hms);
         if (w.more()) {
-          raw_len = c.lens[w.b], raw_new = new_of(w.b), entry = page_entry(w.t0);
+          raw_len = c.lens[w.b], raw_new = new_of(w.b);
+          table.open(c, w.b, w.t0 * kKeys, kKeys / boxes, lane);
           take_q(w);  // the next unit's S may be formed meanwhile
         }
         if (!(ok = mbar_rest_warp(bar(C::B_OFULL), seg & 1, guard, SITE_TREE_SOFTMAX)) || !(ok = meet())) break;
@@ -936,13 +963,15 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
     regs_dec<112>();
     if (!skip) {
       // ---------------------------------------------------------------- e4m3 -> f16 tiles
-      // Warps 8..11 take the K tiles, 12..15 the V tiles: two tiles under way at once.
-      const int kv = (warp - 8) >> 2, tid = (threadIdx.x - 256) & 127;
-      constexpr int PPR = D / 16, NP = PPR;  // 16-byte pieces of an e4m3 row; of a thread
+      // Pairs of warps: 8, 9 and 12, 13 take the K tiles in turn, 10, 11 and 14, 15 the V tiles.  Four tiles are
+      // under way at once, as most of a tile's time is waits (its barriers, the fence): with two groups of four
+      // warps it took 2050 cycles.
+      const int kv = (warp >> 1) & 1, half = (warp - 8) >> 2, tid = threadIdx.x & 63;
+      constexpr int PPR = D / 16, NP = 2 * PPR;  // 16-byte pieces of an e4m3 row; of a thread
       // Piece `sub` of rows k * ROWS + row, k < NP.  Eight lanes read 128 bytes of different banks and write 16-byte
       // units of different banks: at d = 128 (two chunks, 8 pieces a row) lanes 4..7 of eight take the upper half of
       // the neighbouring row, whose swizzle differs in the lowest bit.
-      constexpr int ROWS = 128 / PPR;
+      constexpr int ROWS = 64 / PPR;
       const int sub = tid % PPR;
       const int row = PPR == 8 ? (tid >> 4) * 2 + (((tid >> 2) ^ (tid >> 3)) & 1) : tid / PPR;
       const uint32_t sw = swz_row<C::SWB>(row);
@@ -951,51 +980,56 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
       const uint32_t to0 = to + ((u0 ^ sw) << 4), to1 = to + (((u0 + 1) ^ sw) << 4);
       static_assert(ROWS % 8 == 0, "steps keep the swizzle");
       bool ok = true;
-      int rs = kv % C::NRAW, s = kv, sc = 0;  // slots of the rings
+      int rs = 2 * half + kv, s = 2 * half + kv, sc = half;  // slots of the rings
       uint32_t rpar = 0, spar = 1;
-      for (int left = w.n(); ok && left > 0;) {
-        if (!(ok = mbar_rest_warp(bar(C::B_RFULL + rs), rpar, guard, SITE_TREE_CONVERT))) break;
-        const uint32_t raw = sb + C::OFF_RAW + rs * C::RAW, dst = sb + C::OFF_T + s * C::TILE;
-        uint4 x[NP];
+      int skip_tiles = half;  // the other pair's, before the next of this one's
+      for (; ok && w.more(); w.next(c, hms)) {
+        const int n = w.n();
+        int j = skip_tiles;
+        for (; j < n; j += 2) {
+          if (!(ok = mbar_rest_warp(bar(C::B_RFULL + rs), rpar, guard, SITE_TREE_CONVERT))) break;
+          const uint32_t raw = sb + C::OFF_RAW + rs * C::RAW, dst = sb + C::OFF_T + s * C::TILE;
+          uint4 x[NP];
 #pragma unroll
-        for (int k = 0; k < NP; ++k) x[k] = ld_shared_v4(raw + (k * ROWS + row) * D + sub * 16);
-        int ek = 0, ev = 0;
-        if (kv == 0) {
-          const uint8_t* exps = smem + C::OFF_RAW + rs * C::RAW + 128 * D;
-          ek = exps[tid], ev = exps[128 + tid];
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(C::B_REMPTY + rs));  // the next tile may come while this one is converted
-        if (!(ok = mbar_rest_warp(bar(C::B_EMPTY + s), spar, guard, SITE_TREE_CONVERT))) break;
-        if (kv == 0) {
-          // The tile's scales, for the softmax warps.  This slot held the K tile NSLOT / 2 tiles ago, whose S is
-          // done; so the P of NSB tiles before that was used, and the softmax is past it: the NSLOT / 2 + NSB - 1
-          // tiles it may still read are not overwritten.
-          float* scale = reinterpret_cast<float*>(smem + C::OFF_SCALE) + sc * 384 + tid;
-          // (a row that holds NaN has NaN elements: its scale is 1)
-          scale[0] = ek == kExpNaN ? 1.f : __int_as_float(ek << 23);
-          scale[128] = ev == kExpNaN ? 1.f : __int_as_float(ev << 23);
-          scale[256] = ev == kExpNaN ? 0.f : static_cast<float>(ev - 127);
-          if (++sc == C::NSC) sc = 0;
-        }
+          for (int k = 0; k < NP; ++k) x[k] = ld_shared_v4(raw + (k * ROWS + row) * D + sub * 16);
+          int ek = 0, ev = 0;
+          if (kv == 0) {
+            const uint16_t* exps = reinterpret_cast<const uint16_t*>(smem + C::OFF_RAW + rs * C::RAW + 128 * D);
+            ek = exps[tid], ev = exps[64 + tid];  // two keys' each
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(C::B_REMPTY + rs));  // the next tile may come while this one is converted
+          if (!(ok = mbar_rest_warp(bar(C::B_EMPTY + s), spar, guard, SITE_TREE_CONVERT))) break;
+          if (kv == 0) {
+            // The tile's scales, for the softmax warps.  This slot held the K tile NSLOT / 2 tiles ago, whose S is
+            // done; so the P of NSB tiles before that was used, and the softmax is past it: the NSLOT / 2 + NSB - 1
+            // tiles it may still read are not overwritten.
+            float2* scale = reinterpret_cast<float2*>(smem + C::OFF_SCALE + sc * 1536) + tid;
+            // (a row that holds NaN has NaN elements: its scale is 1)
+            auto power = [](int e) { return e == kExpNaN ? 1.f : __int_as_float(e << 23); };
+            auto exponent = [](int e) { return e == kExpNaN ? 0.f : static_cast<float>(e - 127); };
+            scale[0] = make_float2(power(ek & 255), power(ek >> 8));
+            scale[64] = make_float2(power(ev & 255), power(ev >> 8));
+            scale[128] = make_float2(exponent(ev & 255), exponent(ev >> 8));
+            if ((sc += 2) >= C::NSC) sc -= C::NSC;
+          }
 #pragma unroll
-        for (int k = 0; k < NP; ++k) {
-          const uint32_t w4[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-          uint32_t o[8];
+          for (int k = 0; k < NP; ++k) {
+            const uint32_t w4[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+            uint32_t o[8];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) e4m3x4_to_f16x4(w4[q], o[2 * q], o[2 * q + 1]);
-          st_shared_v4(dst + to0 + k * ROWS * C::SWB, make_uint4(o[0], o[1], o[2], o[3]));
-          st_shared_v4(dst + to1 + k * ROWS * C::SWB, make_uint4(o[4], o[5], o[6], o[7]));
+            for (int q = 0; q < 4; ++q) e4m3x4_to_f16x4(w4[q], o[2 * q], o[2 * q + 1]);
+            st_shared_v4(dst + to0 + k * ROWS * C::SWB, make_uint4(o[0], o[1], o[2], o[3]));
+            st_shared_v4(dst + to1 + k * ROWS * C::SWB, make_uint4(o[4], o[5], o[6], o[7]));
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(C::B_FULL + s));
+          if ((rs += 4) >= C::NRAW) rs -= C::NRAW, rpar ^= 1;
+          if ((s += 4) >= C::NSLOT) s -= C::NSLOT, spar ^= 1;
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(C::B_FULL + s));
-        if ((rs += 2) >= C::NRAW) rs -= C::NRAW, rpar ^= 1;
-        if ((s += 2) >= C::NSLOT) s -= C::NSLOT, spar ^= 1;
-        if (--left == 0) {
-          w.next(c, hms);
-          left = w.more() ? w.n() : 0;
-        }
+        if (!ok) break;
+        skip_tiles = j - n;
       }
     }
   }
