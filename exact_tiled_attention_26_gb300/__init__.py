@@ -14,7 +14,6 @@ from __future__ import annotations
 import ctypes
 import math
 import os
-import typing
 
 __all__ = [
     "FA_OK", "FA_ERR_INVALID_ARG", "FA_ERR_UNSUPPORTED", "FA_ERR_CUDA", "FA_ERR_TIMEOUT", "FA_ERR_WORKSPACE",
@@ -276,8 +275,11 @@ def fa_fwd_tree(Q, cache, O, L, B, H, T, table, table_cols, table_stride, lens, 
                            tree_stride, scale, workspace, workspace_bytes, stream)
 
 
+_Strides = _ll * 3
+
+
 def _ll3(strides):
-    return None if strides is None else (_ll * 3)(*strides)
+    return None if strides is None else _Strides(*strides)
 
 
 def check(status, what=""):
@@ -378,245 +380,15 @@ def attention_fwd_bwd_host(q, k, v, do, causal=False, scale=None, window=0, head
 
 # ------------------------------------------------------------------ around the attention
 
-_UNSET = ctypes.c_size_t(-1).value
+# KVCache, new_cache, qk_norm_rope, qk_norm_rope_backward, cache_write, cache_read, attention_tree and tree_words live
+# in operators.py, which imports PyTorch: loaded on first use, so that the binding itself does not need it.
+_OPERATORS = ("KVCache", "new_cache", "qk_norm_rope", "qk_norm_rope_backward", "cache_write", "cache_read",
+              "attention_tree", "tree_words", "_cache_args")
 
 
-def _on_device(device):
-    """The library launches on the current device: make it `device` for the call."""
-    import contextlib
-
-    import torch
-    return contextlib.nullcontext() if torch.cuda.current_device() == device.index else torch.cuda.device(device)
-
-
-def _ptr(t):
-    return None if t is None or t.numel() == 0 else t.data_ptr()
-
-
-def _check_rows(name, t, like=None):
-    """bf16 CUDA tensor [B,H,N,d] of any row strides the kernels take (elements of a row contiguous)."""
-    import torch
-    if t.dtype != torch.bfloat16 or not t.is_cuda or t.dim() != 4:
-        raise ValueError(f"{name}: expected a bf16 CUDA tensor of shape [B, H, N, d]")
-    if t.numel() and t.shape[3] > 1 and t.stride(3) != 1:
-        raise ValueError(f"{name}: the elements of a row must be contiguous")
-    if like is not None and (t.shape != like.shape or t.device != like.device):
-        raise ValueError(f"{name}: expected shape {tuple(like.shape)} on {like.device}")
-
-
-def _check_ints(name, t, shape, device):
-    import torch
-    if t.dtype != torch.int32 or t.device != device or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous int32 tensor of shape {tuple(shape)} on {device}")
-
-
-def _norm_args(q, k, q_weight, k_weight, cos, sin, positions):
-    """Checks of qk_norm_rope and its gradients; (bf16 weights, rope, rows of the tables)."""
-    import torch
-    _check_rows("q", q)
-    _check_rows("k", k)
-    B, H, N, d = q.shape
-    if (k.shape[0], k.shape[2], k.shape[3]) != (B, N, d) or k.device != q.device:
-        raise ValueError("k must be [B, Hk, N, d] with the B, N and d of q, on its device")
-    types = set()
-    for w in (q_weight, k_weight):
-        if w is not None:
-            if w.shape != (d,) or w.dtype not in (torch.float32, torch.bfloat16) or w.device != q.device or \
-                    not w.is_contiguous():
-                raise ValueError("weights must be contiguous fp32 or bf16 tensors [d] on q's device")
-            types.add(w.dtype)
-    if len(types) > 1:
-        raise ValueError("both weights must have one type")
-    if (cos is None) != (sin is None):
-        raise ValueError("cos and sin come together")
-    rope = rows = 0
-    if cos is not None:
-        for t in (cos, sin):
-            if t.dtype != torch.float32 or t.dim() != 2 or t.shape != cos.shape or t.device != q.device or \
-                    not t.is_contiguous():
-                raise ValueError("cos and sin must be contiguous fp32 tensors [positions, rope / 2] on q's device")
-        rows, rope = cos.shape[0], 2 * cos.shape[1]
-    if positions is not None:
-        if cos is None:
-            raise ValueError("positions need the cos and sin tables")
-        _check_ints("positions", positions, (B, N), q.device)
-    return torch.bfloat16 in types, rope, rows
-
-
-def qk_norm_rope(q, k, q_weight=None, k_weight=None, cos=None, sin=None, positions=None, eps=1e-6, interleaved=False):
-    """RMS norm of each head of bf16 q [B,H,N,d] and k [B,Hk,N,d] (any strides with contiguous rows, e.g. the
-    transposed view of a projection's output), then rotation by position; contiguous bf16 [B,H,N,d], [B,Hk,N,d].
-
-    cos, sin: fp32 [positions, rope/2]; positions: int32 [B,N], default 0..N-1 (a negative one marks a padding row,
-    which comes back zero); interleaved: pairs (2i, 2i+1) instead of (i, i + rope/2).  See fa_qk_norm_rope."""
-    import torch
-    bf16, rope, rows = _norm_args(q, k, q_weight, k_weight, cos, sin, positions)
-    B, H, N, d = q.shape
-    Hk = k.shape[1]
-    qo = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    ko = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-    with _on_device(q.device):
-        check(fa_qk_norm_rope(_ptr(q), _ptr(k), _ptr(qo), _ptr(ko), q.stride()[:3], k.stride()[:3], _ptr(q_weight),
-                              _ptr(k_weight), bf16, _ptr(cos), _ptr(sin), rope, rows, interleaved, _ptr(positions), B, H,
-                              Hk, N, d, eps, _stream_handle(q.device)), "fa_qk_norm_rope")
-    return qo, ko
-
-
-def qk_norm_rope_backward(q, k, dq_out, dk_out, q_weight=None, k_weight=None, cos=None, sin=None, positions=None,
-                          eps=1e-6, interleaved=False, workspace=None):
-    """dq, dk (in the layout of q and k) and the weights' gradients (None without a weight) of qk_norm_rope, from its
-    inputs and the gradients of its outputs."""
-    import torch
-    bf16, rope, rows = _norm_args(q, k, q_weight, k_weight, cos, sin, positions)
-    _check_rows("dq_out", dq_out, q)
-    _check_rows("dk_out", dk_out, k)
-    B, H, N, d = q.shape
-    Hk = k.shape[1]
-    dq, dk = torch.empty_like(q), torch.empty_like(k)
-    dqw, dkw = (None if w is None else torch.empty_like(w) for w in (q_weight, k_weight))
-    ws_bytes = fa_qk_norm_rope_bwd_workspace_size(B, H, Hk, N, d)
-    if ws_bytes == _UNSET:
-        check(FA_ERR_UNSUPPORTED, "fa_qk_norm_rope_bwd_workspace_size")
-    if (dqw is not None or dkw is not None) and (
-            workspace is None or workspace.numel() * workspace.element_size() < ws_bytes):
-        workspace = torch.empty(max(ws_bytes, 16), dtype=torch.uint8, device=q.device)
-    n = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    with _on_device(q.device):
-        check(fa_qk_norm_rope_bwd(_ptr(q), _ptr(k), _ptr(dq_out), _ptr(dk_out), _ptr(dq), _ptr(dk), q.stride()[:3],
-                                  k.stride()[:3], dq_out.stride()[:3], dk_out.stride()[:3], dq.stride()[:3],
-                                  dk.stride()[:3], _ptr(q_weight), _ptr(k_weight), _ptr(dqw), _ptr(dkw), bf16, _ptr(cos),
-                                  _ptr(sin), rope, rows, interleaved, _ptr(positions), B, H, Hk, N, d, eps,
-                                  _ptr(workspace), n, _stream_handle(q.device)), "fa_qk_norm_rope_bwd")
-    return dq, dk, dqw, dkw
-
-
-class KVCache(typing.NamedTuple):
-    """A paged cache: k, v [pages, Hk, page_size, d], bf16, or float8_e4m3fn with one exponent byte per row in k_exp,
-    v_exp (uint8 [pages, Hk, page_size]; a row's scale is 2^(byte - 127))."""
-    k: object
-    v: object
-    k_exp: object = None
-    v_exp: object = None
-
-
-def new_cache(pages, heads, page_size, d, dtype=None, device=None):
-    """A KVCache of zeros; dtype: torch.bfloat16 (the default) or torch.float8_e4m3fn."""
-    import torch
-    dtype = torch.bfloat16 if dtype is None else dtype
-    if dtype not in (torch.bfloat16, torch.float8_e4m3fn):
-        raise ValueError("a cache is bf16 or float8_e4m3fn")
-    device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
-    shape = (pages, heads, page_size, d)
-    if dtype == torch.bfloat16:
-        return KVCache(*(torch.zeros(shape, dtype=dtype, device=device) for _ in range(2)))
-    return KVCache(*(torch.zeros(shape, dtype=torch.uint8, device=device).view(dtype) for _ in range(2)),
-                   *(torch.zeros(shape[:3], dtype=torch.uint8, device=device) for _ in range(2)))
-
-
-def _cache_args(cache, table, lens, n_new):
-    """Checks of a cache and its table; (fa_cache, arguments of the table)."""
-    import torch
-    k, v = cache.k, cache.v
-    for t in (k, v):
-        if t.dim() != 4 or t.dtype not in (torch.bfloat16, torch.float8_e4m3fn) or not t.is_cuda or \
-                not t.is_contiguous() or t.shape != k.shape or t.dtype != k.dtype or t.device != k.device:
-            raise ValueError("a cache's k and v must be contiguous bf16 or float8_e4m3fn CUDA tensors "
-                             "[pages, Hk, page_size, d] of one type and device")
-    fp8 = k.dtype == torch.float8_e4m3fn
-    for t in (cache.k_exp, cache.v_exp):
-        if (t is not None) != fp8:
-            raise ValueError("an e4m3 cache has exponent bytes k_exp and v_exp, a bf16 cache has none")
-        if fp8 and (t.dtype != torch.uint8 or t.shape != k.shape[:3] or t.device != k.device or not t.is_contiguous()):
-            raise ValueError("exponent bytes must be contiguous uint8 tensors [pages, Hk, page_size] on the cache's device")
-    if table.dim() != 2 or table.dtype != torch.int32 or table.device != k.device or \
-            (table.shape[1] > 1 and table.stride(1) != 1):
-        raise ValueError("the page table must be an int32 tensor [B, columns] on the cache's device, rows contiguous")
-    B = table.shape[0]
-    _check_ints("lens", lens, (B,), k.device)
-    if n_new is not None:
-        _check_ints("n_new", n_new, (B,), k.device)
-    pages, hk, page_size, d = k.shape
-    c = fa_cache(_ptr(k), _ptr(v), _ptr(cache.k_exp), _ptr(cache.v_exp), FA_CACHE_E4M3 if fp8 else FA_CACHE_BF16, pages,
-                 hk, page_size, d)
-    return c, (_ptr(table), table.shape[1], table.stride(0), _ptr(lens))
-
-
-def cache_write(cache, k, v, table, lens, n_new=None):
-    """Writes bf16 k, v [B,Hk,T,d] (any strides with contiguous rows) into the cache: token t < n_new[b] (default T) of
-    sequence b goes to row lens[b] - n_new[b] + t of its pages table[b].  lens counts the new tokens."""
-    _check_rows("k", k)
-    _check_rows("v", v, k)
-    c, tab = _cache_args(cache, table, lens, n_new)
-    B, hk, T, d = k.shape
-    if (B, hk, d) != (table.shape[0], c.Hk, c.d) or k.device != cache.k.device:
-        raise ValueError("k and v must be [B, Hk, T, d] with the table's B and the cache's Hk and d, on its device")
-    with _on_device(k.device):
-        check(fa_cache_write(c, _ptr(k), _ptr(v), k.stride()[:3], v.stride()[:3], B, T, *tab, _ptr(n_new),
-                             _stream_handle(k.device)), "fa_cache_write")
-
-
-def cache_read(cache, table, lens, length):
-    """k, v: rows 0 .. length-1 of every sequence as contiguous bf16 [B,Hk,length,d], zero behind lens[b]."""
-    import torch
-    c, tab = _cache_args(cache, table, lens, None)
-    shape = (table.shape[0], c.Hk, length, c.d)
-    k, v = (torch.empty(shape, dtype=torch.bfloat16, device=cache.k.device) for _ in range(2))
-    with _on_device(k.device):
-        check(fa_cache_read(c, _ptr(k), _ptr(v), shape[0], length, *tab, _stream_handle(k.device)), "fa_cache_read")
-    return k, v
-
-
-def tree_words(parents):
-    """The `tree` of attention_tree from draft trees: parents is a CPU integer tensor or nested list [T] or [B,T] with
-    the index of the token that each token follows (smaller than its own), or -1 at a root.  Returns int64 words
-    [T, W] or [B, T, W] on the CPU: bit j of a token's words is set for itself and its ancestors."""
-    import torch
-    p = torch.as_tensor(parents)
-    rows = (p if p.dim() == 2 else p[None]).tolist()
-    T = p.shape[-1]
-    W = (T + 63) // 64
-    out = []
-    for row in rows:
-        seen = []
-        for t, at in enumerate(row):
-            if not -1 <= at < t:
-                raise ValueError("a token's parent must come before it (-1: none)")
-            seen.append((seen[at] if at >= 0 else 0) | 1 << t)
-        words = [[(s >> (64 * w)) & (2 ** 64 - 1) for w in range(W)] for s in seen]
-        out.append([[u - 2 ** 64 if u >= 2 ** 63 else u for u in ws] for ws in words])
-    res = torch.tensor(out, dtype=torch.int64).reshape(len(rows), T, W)
-    return res if p.dim() == 2 else res[0]
-
-
-def attention_tree(q, cache, table, lens, tree=None, n_new=None, scale=None, workspace=None):
-    """O [B,H,T,d], L [B,H,T] of T drafted tokens per sequence (T = 1: a decoded token) over the cache that holds their
-    own keys and values too: q bf16 contiguous [B,H,T,d], H a multiple of the cache's heads.  tree: int64 words [B,T,W]
-    or, for one tree, [T,W], W = ceil(T/64) (tree_words); None: token t sees tokens 0..t.  See fa_fwd_tree."""
-    import torch
-    if q.dtype != torch.bfloat16 or not q.is_cuda or not q.is_contiguous() or q.dim() != 4:
-        raise ValueError("q: expected a contiguous bf16 CUDA tensor of shape [B, H, T, d]")
-    c, tab = _cache_args(cache, table, lens, n_new)
-    B, H, T, d = q.shape
-    if (B, d) != (table.shape[0], c.d) or q.device != cache.k.device:
-        raise ValueError("q must be [B, H, T, d] with the table's B and the cache's d, on its device")
-    if H and (c.Hk == 0 or H % c.Hk):
-        raise ValueError("the heads of q must be a multiple of the cache's")
-    stride, W = 0, (T + 63) // 64
-    if tree is not None:
-        if tree.dtype != torch.int64 or tree.device != q.device or not tree.is_contiguous() or \
-                tuple(tree.shape) not in ((T, W), (B, T, W)):
-            raise ValueError(f"tree must be a contiguous int64 tensor [{B}, {T}, {W}] or [{T}, {W}] on q's device")
-        stride = T * W if tree.dim() == 3 else 0
-    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    o = torch.empty_like(q)
-    lse = torch.empty((B, H, T), dtype=torch.float32, device=q.device)
-    ws_bytes = fa_fwd_tree_workspace_size(B, H, c.Hk, T, d)
-    if ws_bytes == _UNSET:
-        check(FA_ERR_INVALID_ARG, "fa_fwd_tree_workspace_size")
-    if workspace is None or workspace.numel() * workspace.element_size() < ws_bytes:
-        workspace = torch.empty(max(ws_bytes, 16), dtype=torch.uint8, device=q.device)
-    with _on_device(q.device):
-        check(fa_fwd_tree(_ptr(q), c, _ptr(o), _ptr(lse), B, H, T, *tab, _ptr(n_new), _ptr(tree), stride, scale,
-                          workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream_handle(q.device)),
-              "fa_fwd_tree")
-    return o, lse
+def __getattr__(name):
+    if name not in _OPERATORS:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    from . import operators
+    globals().update((n, getattr(operators, n)) for n in _OPERATORS)
+    return globals()[name]

@@ -8,8 +8,9 @@ from __future__ import annotations
 
 import torch
 
-from . import attention_backward, attention_forward, qk_norm_rope_backward
-from . import qk_norm_rope as _qk_norm_rope
+from . import attention_backward, attention_forward
+from .operators import qk_norm_rope as _qk_norm_rope
+from .operators import qk_norm_rope_backward
 
 
 class FlashAttentionFunction(torch.autograd.Function):
