@@ -26,8 +26,14 @@ namespace fa {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kHeads = 4;               // heads per lane group and step
-constexpr int kMaxBlocks = 152 * 4;     // per tensor
+constexpr int kHeads = 4;  // heads per lane group and step
+// Blocks resident on an SM: the grid is that many blocks (shared out between q and k by
+// their work), each of which runs to the end.  Measured at 1 x 32 x 8192 x 128, q and k
+// (heads per step, blocks): forward 49.8 us at (4, 4), 58.8 at (2, 4), 74 at (8, 2);
+// gradients 76.7 us at (4, 3), 85.7 at (2, 3), 108 at (4, 2); loading the next step's rows
+// ahead 52.7 and 83 at best; twice the blocks 50.1 and 80.1.
+template <bool GRAD>
+constexpr int kBlocks = GRAD ? 3 : 4;
 
 struct RowStrides {
   long long b, h, n;
@@ -52,6 +58,13 @@ struct NormArgs {
   float eps;
 };
 
+FA_DEV uint4 ld_stream(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
 FA_DEV void unpack8(uint4 v, float* f) {
   const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -126,7 +139,7 @@ FA_DEV void load_angles(Angles& a, const NormArgs& p, int position, int col) {
 
 // GRAD: gradients.  LPR = D / 8 lanes per row.
 template <int D, bool GRAD>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_constant__ NormArgs p) {
+__global__ void __launch_bounds__(kThreads, kBlocks<GRAD>) norm_rope_kernel(const __grid_constant__ NormArgs p) {
   constexpr int LPR = D / 8, GPW = 32 / LPR;  // lane groups per warp
   const bool is_k = blockIdx.x >= static_cast<unsigned>(p.grid_q);
   const NormTensor& t = p.t[is_k ? 1 : 0];
@@ -138,6 +151,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
   const unsigned ngroups = nblocks * (kThreads / 32) * GPW;
   const unsigned hblocks = (t.H + kHeads - 1) / kHeads;
 
+  pdl_wait();
   float w[8], wo[8];  // weights of this lane's elements and of the ones they pair with
   load_weight(t.w, p.w_bf16, col, w);
   // half-split pairs: the lane of the same row that holds the other half's elements
@@ -160,16 +174,20 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
     uint4 xv[kHeads], gv[kHeads];
 #pragma unroll
     for (int i = 0; i < kHeads; ++i)
-      xv[i] = i < nh ? *reinterpret_cast<const uint4*>(x + i * t.sx.h) : make_uint4(0, 0, 0, 0);
+      xv[i] = i < nh ? ld_stream(x + i * t.sx.h) : make_uint4(0, 0, 0, 0);
     if constexpr (GRAD) {
       const __nv_bfloat16* dz = t.dz + b * t.sdz.b + n * t.sdz.n + h0 * t.sdz.h + col;
 #pragma unroll
       for (int i = 0; i < kHeads; ++i)
-        gv[i] = i < nh ? *reinterpret_cast<const uint4*>(dz + i * t.sdz.h) : make_uint4(0, 0, 0, 0);
+        gv[i] = i < nh ? ld_stream(dz + i * t.sdz.h) : make_uint4(0, 0, 0, 0);
     }
     const int position = p.pos != nullptr && live ? p.pos[bn] : static_cast<int>(n);
     Angles a;
     load_angles(a, p, live ? position : 0, position < 0 ? D : col);
+    if constexpr (!GRAD) {  // the weights are the same for all heads of the step
+#pragma unroll
+      for (int e = 0; e < 8; ++e) a.c[e] *= w[e], a.s[e] *= p.interleaved ? w[e ^ 1] : wo[e];
+    }
     __nv_bfloat16* out = t.out + b * t.so.b + n * t.so.n + h0 * t.so.h + col;
 #pragma unroll
     for (int i = 0; i < kHeads; ++i) {
@@ -189,14 +207,12 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
       unpack8(src, u);
       unpack8(ov, o);
       if constexpr (!GRAD) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) u[e] = u[e] * r * w[e], o[e] = o[e] * r * wo[e];
         if (p.interleaved) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) o[e] = u[e ^ 1];
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) res[e] = fmaf(u[e], a.c[e], o[e] * a.s[e]);
+        for (int e = 0; e < 8; ++e) res[e] = r * fmaf(u[e], a.c[e], o[e] * a.s[e]);
       } else {
         if (p.interleaved) {
 #pragma unroll
@@ -273,10 +289,21 @@ __global__ void __launch_bounds__(256) dw_sum_kernel(const __grid_constant__ DwA
 long long item_count(int B, int H, int N) {
   return static_cast<long long>(B) * N * ((H + kHeads - 1) / kHeads);
 }
-int blocks_for(long long items, int d) {
-  const long long per_block = (kThreads / 32) * (32 / (d / 8));
-  const long long n = (items + per_block - 1) / per_block;
-  return static_cast<int>(n < kMaxBlocks ? n : kMaxBlocks);
+// Blocks for q (blocks[0]) and k: what the items need, or all that are resident, shared
+// out by items.
+template <bool GRAD>
+void grid_for(int B, int Hq, int Hk, int N, int d, int blocks[2]) {
+  const long long per_block = (kThreads / 32) * (32 / (d / 8)), most = 152 * kBlocks<GRAD>;
+  const long long iq = item_count(B, Hq, N), ik = item_count(B, Hk, N);
+  long long nq = (iq + per_block - 1) / per_block, nk = (ik + per_block - 1) / per_block;
+  if (nq + nk > most) {
+    const long long all = nq + nk, wq = nq;
+    nq = nq * most / all;
+    if (nq == 0 && wq > 0) nq = 1;
+    if (nq == most && nk > 0) nq = most - 1;
+    nk = nk > 0 ? most - nq : 0;
+  }
+  blocks[0] = static_cast<int>(nq), blocks[1] = static_cast<int>(nk);
 }
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
@@ -311,12 +338,12 @@ fa_status check_norm(int B, int Hq, int Hk, int N, int d, float eps, const float
 
 template <bool GRAD>
 cudaError_t launch_norm(const NormArgs& p, int grid, int d, cudaStream_t s) {
+  const dim3 g(grid), t(kThreads);
   switch (d) {
-    case 32: norm_rope_kernel<32, GRAD><<<grid, kThreads, 0, s>>>(p); break;
-    case 64: norm_rope_kernel<64, GRAD><<<grid, kThreads, 0, s>>>(p); break;
-    default: norm_rope_kernel<128, GRAD><<<grid, kThreads, 0, s>>>(p); break;
+    case 32: return launch_pdl(norm_rope_kernel<32, GRAD>, g, t, 0, s, p);
+    case 64: return launch_pdl(norm_rope_kernel<64, GRAD>, g, t, 0, s, p);
+    default: return launch_pdl(norm_rope_kernel<128, GRAD>, g, t, 0, s, p);
   }
-  return cudaGetLastError();
 }
 
 }  // namespace
@@ -353,8 +380,8 @@ fa_status fa_qk_norm_rope(const void* Q, const void* K, void* Qout, void* Kout, 
     read_strides(nullptr, B, H[i], N, d, &t.so);
     t.H = H[i];
     t.items = static_cast<unsigned>(item_count(B, H[i], N));
-    blocks[i] = blocks_for(t.items, d);
   }
+  grid_for<false>(B, Hq, Hk, N, d, blocks);
   p.cos = cos, p.sin = sin, p.pos = positions;
   p.N = N, p.rope = rope, p.table_rows = table_rows, p.interleaved = interleaved ? 1 : 0;
   p.w_bf16 = weight_bf16 ? 1 : 0, p.grid_q = blocks[0], p.eps = eps;
@@ -363,8 +390,9 @@ fa_status fa_qk_norm_rope(const void* Q, const void* K, void* Qout, void* Kout, 
 
 size_t fa_qk_norm_rope_bwd_workspace_size(int B, int Hq, int Hk, int N, int d) {
   if (B < 0 || Hq < 0 || Hk < 0 || N < 0 || (d != 32 && d != 64 && d != 128)) return static_cast<size_t>(-1);
-  return (static_cast<size_t>(blocks_for(item_count(B, Hq, N), d)) + blocks_for(item_count(B, Hk, N), d)) * d *
-         sizeof(float);
+  int blocks[2];
+  grid_for<true>(B, Hq, Hk, N, d, blocks);
+  return (static_cast<size_t>(blocks[0]) + blocks[1]) * d * sizeof(float);
 }
 
 fa_status fa_qk_norm_rope_bwd(const void* Q, const void* K, const void* dQout, const void* dKout, void* dQ, void* dK,
@@ -406,6 +434,7 @@ fa_status fa_qk_norm_rope_bwd(const void* Q, const void* K, const void* dQout, c
     void* dx[2] = {dQ, dK};
     const void* w[2] = {q_weight, k_weight};
     float* part = static_cast<float*>(workspace);
+    grid_for<true>(B, Hq, Hk, N, d, r.blocks);
     for (int i = 0; i < 2; ++i) {
       NormTensor& t = p.t[i];
       t.x = static_cast<const __nv_bfloat16*>(x[i]);
@@ -414,7 +443,6 @@ fa_status fa_qk_norm_rope_bwd(const void* Q, const void* K, const void* dQout, c
       t.w = w[i];
       t.H = H[i];
       t.items = static_cast<unsigned>(item_count(B, H[i], N));
-      r.blocks[i] = blocks_for(t.items, d);
       t.dw_part = dw[i] != nullptr ? part : nullptr;
       r.part[i] = part;
       if (part != nullptr) part += static_cast<size_t>(r.blocks[i]) * d;
