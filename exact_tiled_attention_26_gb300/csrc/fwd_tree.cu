@@ -173,26 +173,53 @@ struct TableWindow {
   }
 };
 
-// Exclusive prefix of one int per thread over the block; *total for all.  NT threads.
-template <int NT>
-FA_DEV long long block_prefix(long long v, long long* scratch, long long* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  long long x = v;
-#pragma unroll
-  for (int k = 1; k < 32; k <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, x, k);
-    if (lane >= k) x += y;
+// The run of one of `ctas` CTAs: its first place `lo`, its places `mine`, the places of
+// every full run, and where it begins.  Every warp finds it by itself, each lane with a
+// share of the sequences (all call it; the result is the same in every lane).
+struct Run {
+  long long lo, mine, run;
+  Walk w;
+};
+FA_DEV Run find_run(const CacheView& c, int B, int hms, int cta, int ctas, int lane) {
+  const int per = (B + 31) / 32, b0 = min(lane * per, B), b1 = min(b0 + per, B);
+  long long sum = 0;
+  int first = 0;
+  for (int b = b0; b < b1; ++b) {
+    const int n = tiles_of(c, b) + kUnitCost;
+    if (b == b0) first = n;
+    sum += n;
   }
-  if (lane == 31) scratch[warp] = x;
-  __syncthreads();
-  long long before = 0, all = 0;
-#pragma unroll
-  for (int w = 0; w < NT / 32; ++w) {
-    if (w < warp) before += scratch[w];
-    all += scratch[w];
+  long long upto = sum;
+#pragma unroll 1
+  for (int k = 1; k < min(B, 32); k <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, upto, k);
+    if (lane >= k) upto += y;
   }
-  *total = all;
-  return before + x - v;
+  // (lanes behind the last sequence have their neighbour's sum only after all steps: take the last one's)
+  const long long total = __shfl_sync(0xffffffffu, upto, (B - 1) / per) * hms, before = (upto - sum) * hms;
+  Run r;
+  r.run = quotient(total + ctas - 1, ctas);
+  r.lo = r.run * cta;
+  r.mine = total - r.lo < r.run ? total - r.lo : r.run;
+  r.w = Walk{0, 0, 0, 0, 0, 0};
+  if (r.mine <= 0) return r;
+  // the lane with the sequence of the run's first place
+  const bool here = b0 < b1 && r.lo >= before && r.lo < before + sum * hms;
+  int b = b0, hm = 0, place = 0, places = first;
+  if (here) {
+    long long at = before;
+    while (r.lo >= at + static_cast<long long>(places) * hms) {
+      at += static_cast<long long>(places) * hms;
+      places = tiles_of(c, ++b) + kUnitCost;
+    }
+    hm = static_cast<int>(quotient(r.lo - at, places));
+    place = static_cast<int>(r.lo - at - static_cast<long long>(hm) * places);
+  }
+  const int src = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
+  b = __shfl_sync(0xffffffffu, b, src), hm = __shfl_sync(0xffffffffu, hm, src);
+  place = __shfl_sync(0xffffffffu, place, src), places = __shfl_sync(0xffffffffu, places, src);
+  r.w = Walk{b, hm, max(place - kUnitCost, 0), places - kUnitCost, max(kUnitCost - place, 0), r.mine};
+  return r;
 }
 
 // 32 bits of a token's mask from draft index d0 on (bits below index 0 and behind the
@@ -341,10 +368,8 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
   auto bar = [&](int i) -> uint32_t { return sb + C::OFF_BAR + 8 * i; };
   uint32_t* misc = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
-  volatile int* start = reinterpret_cast<volatile int*>(misc + 2);  // b, hm and place in the unit, of the run's first place
   uint32_t* bad_rows = misc + 8;                                    // 4 words
   volatile uint32_t* bad_stage = misc + 12;                         // 8 words
-  long long* scratch = reinterpret_cast<long long*>(smem + C::OFF_ROWS);
   const Guard guard{p.status, abort_flag};
   const CacheView& c = p.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -367,43 +392,12 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
   }
   pdl_wait();  // everything from here on may be an earlier kernel's output
   if (threadIdx.x == 64) *abort_flag = (*reinterpret_cast<volatile int*>(p.status) != 0);
-  // this CTA's run
-  long long lo, mine, run;
-  {
-    const int per = (p.B + C::NTHREADS - 1) / C::NTHREADS, b0 = threadIdx.x * per, b1 = min(b0 + per, p.B);
-    long long sum = 0, total = 0;
-    for (int b = b0; b < b1; ++b) sum += tiles_of(c, b) + kUnitCost;
-    const long long before = block_prefix<C::NTHREADS>(sum, scratch, &total);
-    total *= hms;
-    run = quotient(total + gridDim.x - 1, gridDim.x);
-    lo = run * blockIdx.x;
-    mine = total - lo < run ? total - lo : run;
-    if (mine > 0 && lo >= before * hms && lo < (before + sum) * hms) {
-      long long at = before * hms;
-      int b = b0;
-      for (;; ++b) {
-        const long long n = static_cast<long long>(tiles_of(c, b) + kUnitCost) * hms;
-        if (lo < at + n) break;
-        at += n;
-      }
-      const int places = tiles_of(c, b) + kUnitCost;
-      const int hm = static_cast<int>(quotient(lo - at, places));
-      start[0] = b;
-      start[1] = hm;
-      start[2] = static_cast<int>(lo - at - static_cast<long long>(hm) * places);
-    }
-  }
+  const Run mine = find_run(c, p.B, hms, blockIdx.x, gridDim.x, lane);
+  Walk w = mine.w;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = misc[0];
-  Walk w{0, 0, 0, 0, 0, 0};
-  if (mine > 0) {
-    w.b = start[0], w.hm = start[1];
-    w.t0 = max(start[2] - kUnitCost, 0), w.cost = max(kUnitCost - start[2], 0);
-    w.nt = tiles_of(c, w.b);
-    w.left = mine;
-  }
   const bool skip = *abort_flag != 0 || !w.more();
 
   if (warp < 4) {
@@ -434,11 +428,12 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
           const int y = (tile * kKeys) & (c.page - 1);  // a tile's place in a page of more than a tile
           if (!(ok = mbar_rest_warp(bar(BEMPTY + slot), parity, guard, SITE_TREE_PRODUCER))) break;
           const uint32_t full = bar(BFULL + slot);
+          const uint32_t dst = sb + (FP8 ? C::OFF_RAW + slot * C::RAW : C::OFF_T + slot * C::TILE);
           if constexpr (FP8) {
-            const uint32_t dst = sb + C::OFF_RAW + slot * C::RAW, exps = dst + 128 * D + lane * rb;
             const bool there = issues && z != nowhere;
             const int n_there = __popc(__ballot_sync(0xffffffffu, there));
             if (kv == 0 && issues && !there) {  // no page, no exponents: 2^-127
+              const uint32_t exps = dst + 128 * D + lane * rb;
               for (int k = 0; k < rb; k += 16) {
                 st_shared_v4(exps + k, make_uint4(0u, 0u, 0u, 0u));
                 st_shared_v4(exps + 128 + k, make_uint4(0u, 0u, 0u, 0u));
@@ -460,12 +455,17 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
             }
           } else {
             if (lane == 0) mbar_expect_tx(full, C::TILE);
-            for (int i = 0; i < boxes; ++i) {
-              const int zi = __shfl_sync(0xffffffffu, z, i);
-              if (lane == 0)
+            int zs[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) zs[i] = __shfl_sync(0xffffffffu, z, i);
+            if (lane == 0) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                if (i >= boxes) break;
+#pragma unroll
                 for (int ch = 0; ch < D / C::CE; ++ch)
-                  tma_load_3d(sb + C::OFF_T + slot * C::TILE + ch * 128 * C::SWB + i * rb * C::SWB, map, full, ch * C::CE, y,
-                              zi);
+                  tma_load_3d(dst + ch * 128 * C::SWB + i * rb * C::SWB, map, full, ch * C::CE, y, zs[i]);
+              }
             }
           }
           ++items;
@@ -813,9 +813,9 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
         tc_fence_after();
         const bool whole = at.t0 == 0 && n == at.nt;
         if (at.t0 == 0 && tid == 0) {
-          const long long first = lo + mine - at.left + at.cost;  // the place of the unit's first tile
+          const long long first = mine.lo + mine.mine - at.left + at.cost;  // the place of the unit's first tile
           p.info[static_cast<long long>(at.b) * hms + at.hm] =
-              UnitInfo{static_cast<int>(blockIdx.x), static_cast<int>(quotient(first + at.nt - 1, run))};
+              UnitInfo{static_cast<int>(blockIdx.x), static_cast<int>(quotient(first + at.nt - 1, mine.run))};
         }
         // a NaN score does not move the maximum: where nothing else is seen it is still -inf
         if (lr != lr) ref = lr;
@@ -1221,8 +1221,9 @@ fa_status fa_fwd_tree(const void* Q, const fa_cache* cache, void* O, float* L, i
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&grid, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return FA_ERR_CUDA;
-  // no more CTAs than there can be tiles
-  const long long most = units * ((static_cast<long long>(table_cols) * cache->page_size + kKeys - 1) / kKeys);
+  // no more CTAs than there can be places
+  const long long most =
+      units * ((static_cast<long long>(table_cols) * cache->page_size + kKeys - 1) / kKeys + kUnitCost);
   if (grid > kMaxGrid) grid = kMaxGrid;
   if (most < grid) grid = static_cast<int>(most);
   const bool fp8 = cache->format == FA_CACHE_E4M3;
