@@ -53,6 +53,7 @@ namespace {
 constexpr int kMaxGrid = 152;  // CTAs at most, one per SM
 constexpr int kKeys = 128;     // keys per tile
 constexpr int kUnitCost = 3;   // see Walk
+constexpr int kConvertRegs = 112;
 
 enum : int { SITE_TREE_PRODUCER = 0x501, SITE_TREE_MMA = 0x502, SITE_TREE_SOFTMAX = 0x503, SITE_TREE_CONVERT = 0x504 };
 
@@ -82,13 +83,16 @@ struct TCfg {
   static constexpr int SWB = (D * 2 >= 128) ? 128 : D * 2;
   static constexpr int CE = SWB / 2;
   static constexpr int TILE = 128 * D * 2;
+  // Softmax warpgroups: two share a tile's columns where every row weighs all 128 keys itself.
+  static constexpr int NW = NS == 1 ? 2 : 1;
+  static constexpr int NPAIR = NW == 2 ? 1 : 2;            // pairs of converting warps for K, and for V
   static constexpr int NSLOT = D < 128 ? 8 : FP8 ? 4 : 6;  // 16-bit tiles, K and V in turn
   static constexpr int NRAW = FP8 ? NSLOT : 0;             // e4m3 tiles
-  // K tiles use the even slots of a ring and V tiles the odd ones, and the two pairs of warps that take an e4m3
-  // cache's tiles in turn have slots of their own too (4 divides NSLOT and NRAW).  So each slot's barriers are waited
+  // K tiles use the even slots of a ring and V tiles the odd ones, and pairs of warps that take an e4m3 cache's
+  // tiles in turn have slots of their own too (2 NPAIR divides NSLOT and NRAW).  So each slot's barriers are waited
   // for by one party that sees every phase of them: with a slot shared, a party that is a tile ahead would take the
   // other's phase for its own.
-  static_assert(NSLOT % 2 == 0 && (!FP8 || (NSLOT % 4 == 0 && NRAW % 4 == 0)), "slots of their own");
+  static_assert(NSLOT % 2 == 0 && (!FP8 || (NSLOT % (2 * NPAIR) == 0 && NRAW % (2 * NPAIR) == 0)), "slots of their own");
   static constexpr int RAW = 128 * D + 256;     // with the exponent bytes of its keys (K tiles: and of their values)
   static constexpr int NSB = 2;                 // S buffers in tensor memory
   static constexpr int NPB = D == 128 ? 1 : 2;  // P buffers
@@ -98,11 +102,13 @@ struct TCfg {
   static constexpr int OFF_RAW = OFF_X + (NS > 1 ? 16384 : 0);
   static constexpr int OFF_SCALE = OFF_RAW + NRAW * RAW;  // [NSC][3][128] floats: 2^k of K, 2^k of V, k of V
   static constexpr int OFF_ROWS = OFF_SCALE + NSC * 3 * 128 * 4;  // [3][128] floats
-  static constexpr int OFF_BAR = OFF_ROWS + 3 * 128 * 4;
+  static constexpr int OFF_TOPS = OFF_ROWS + 3 * 128 * 4;         // NW = 2: [2][2][128] floats
+  static constexpr int OFF_BAR = OFF_TOPS + (NW == 2 ? 2048 : 0);
   static constexpr int B_QREADY = 0, B_FULL = 1, B_EMPTY = B_FULL + NSLOT,
                        B_RFULL = B_EMPTY + NSLOT, B_REMPTY = B_RFULL + NRAW, B_SFULL = B_REMPTY + NRAW,
                        B_SFREE = B_SFULL + NSB, B_PFULL = B_SFREE + NSB, B_PFREE = B_PFULL + NPB, B_OFULL = B_PFREE + NPB, B_OFREE = B_OFULL + 1,
-                       B_MEET = B_OFREE + 1, B_SDONE = B_MEET + 1, B_PVDONE = B_SDONE + 1, NBAR = B_PVDONE + 1;
+                       B_MEET = B_OFREE + 1, B_TOP = B_MEET + 1, B_LSUM = B_TOP + (NW == 2 ? 4 : 0),
+                       B_SDONE = B_LSUM + (NW == 2 ? 1 : 0), B_PVDONE = B_SDONE + 1, NBAR = B_PVDONE + 1;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;     // 24 words
   static constexpr int SMEM_USED = OFF_MISC + 96;
   static constexpr int SMEM = (SMEM_USED + 1024 > 120 * 1024) ? SMEM_USED + 1024 : 120 * 1024;
@@ -110,7 +116,11 @@ struct TCfg {
   // an S buffer is free again as soon as its scores are in registers: with P written over S the loop
   // softmax - P V - S - softmax bound the kernel (2 buffers: 2040 cycles a tile at d = 128).
   static constexpr int TM_S0 = 0, TM_P0 = NSB * 128, TM_O = TM_P0 + NPB * 64, TM_Q = TM_O + D, TM_COLS = 512;
-  static constexpr int NTHREADS = FP8 ? 512 : 256;
+  static constexpr int NTHREADS = FP8 ? 512 : 128 + 128 * NW;
+  // setmaxnreg shares of issue, softmax and converting warps (0: none); their sums over the warpgroups stay within
+  // the launch's: 4 x 128 with 512 threads, 3 x 168 with 384
+  static constexpr int R_ISSUE = FP8 ? (NW == 2 ? 64 : 80) : NW == 2 ? 64 : 0;
+  static constexpr int R_SOFT = FP8 ? (NW == 2 ? 168 : 208) : NW == 2 ? 216 : 0;
   static_assert(SMEM <= 232448, "shared memory budget");
   static_assert(TM_Q + D / 2 <= TM_COLS, "tensor memory budget");
 };
@@ -379,10 +389,13 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
   if (threadIdx.x < C::NBAR) {
     const int i = threadIdx.x;
     // one arrival for loads and commits, one for each of four warps elsewhere
-    const bool four = i == C::B_QREADY || i == C::B_OFREE || i == C::B_MEET || (i >= C::B_SFREE && i < C::B_PFREE);
-    // (and of two where the e4m3 tiles are converted)
-    const bool two = FP8 && ((i >= C::B_FULL && i < C::B_EMPTY) || (i >= C::B_REMPTY && i < C::B_SFULL));
-    mbar_init(bar(i), four ? 4 : two ? 2 : 1);
+    const bool four = i == C::B_QREADY || i == C::B_OFREE || i == C::B_MEET || (C::NW == 2 && i == C::B_LSUM);
+    // (of all softmax warps, for the scores read and the weights written)
+    const bool all = i >= C::B_SFREE && i < C::B_PFREE;
+    // (and of two where the e4m3 tiles are converted, and between two softmax warps of the same rows)
+    const bool two = (FP8 && ((i >= C::B_FULL && i < C::B_EMPTY) || (i >= C::B_REMPTY && i < C::B_SFULL))) ||
+                     (i >= C::B_TOP && i < C::B_LSUM);
+    mbar_init(bar(i), four ? 4 : all ? 4 * C::NW : two ? 2 : 1);
     fence_mbar_init();
   }
   if (threadIdx.x < 4) bad_rows[threadIdx.x] = 0u;
@@ -401,7 +414,7 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
   const bool skip = *abort_flag != 0 || !w.more();
 
   if (warp < 4) {
-    if constexpr (FP8) regs_dec<80>();
+    if constexpr (C::R_ISSUE > 0) regs_dec<C::R_ISSUE>();
     if ((warp == 0 || warp == 3) && !skip) {
       // ---------------------------------------------------------------- producers: warp 0 K, warp 3 V
       const int kv = warp == 0 ? 0 : 1;
@@ -535,12 +548,19 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
       }
       mma_commit(bar(C::B_PVDONE));  // every S completed before its P: the end of all UMMAs
     }
-  } else if (warp < 8) {
-    if constexpr (FP8) regs_inc<208>();
+  } else if (warp < 4 + 4 * C::NW) {
+    if constexpr (C::R_SOFT > 0) regs_inc<C::R_SOFT>();
     if (!skip) {
       // ---------------------------------------------------------------- softmax + epilogue
+      // With two warpgroups, warps w and w + 4 have the same rows and each half of the columns.  They agree on a
+      // tile's largest score (B_TOP) and so always have the same reference; the first warpgroup (`lead`) also takes
+      // Q, cleans values and stores the results.
       const int wq = warp & 3, row = wq * 32 + lane;
+      const int wg = C::NW == 2 ? (warp - 4) >> 2 : 0;
+      const bool lead = C::NW == 1 || wg == 0;
+      constexpr int COLS = GR / C::NW;              // columns of a thread
       const int group = row / GR, r_in = row % GR;  // key group, row of the query tile
+      const int col0 = group * GR + wg * COLS;
       const uint32_t tl = tmem + (static_cast<uint32_t>(wq * 32) << 16);
       const int tid = threadIdx.x - 128;
       float* rows = reinterpret_cast<float*>(smem + C::OFF_ROWS);
@@ -550,6 +570,7 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
       bool ok = true;
       int seg = 0, b = 0, pb = 0, vs_slot = 1, sc = 0;  // S buffer, P buffer, slot of V, scales
       uint32_t bpar = 0, pfree = 1, vpar = 0, meet_parity = 0;
+      [[maybe_unused]] uint32_t top_parity = 0;
       // The four softmax warps meet; a wait with a limit.  It does not look at the abort flag, so that
       // either all four pass or none does, and what follows may use plain barriers.
       auto meet = [&]() -> bool {
@@ -588,6 +609,7 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
           mul = __int_as_float((268 - e) << 23);                     // 2^(14 - (e - 127))
           q_scale = p.c_log2 * __int_as_float((e - 14) << 23);
         }
+        if (!lead) return;
 #pragma unroll
         for (int k = 0; k < D / 32; ++k) {
           uint32_t o[16];
@@ -661,20 +683,20 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
           if (!(ok = mbar_rest_warp(bar(C::B_SFULL + b), bpar, guard, SITE_TREE_SOFTMAX))) break;
           tc_fence_after();
           if (warp_live) {
-            uint32_t r[GR];
-            float s[GR];
+            uint32_t r[COLS];
+            float s[COLS];
 #pragma unroll
-            for (int i = 0; i < GR / 32; ++i) tmem_ld32(tl + C::TM_S0 + b * 128 + group * GR + 32 * i, r + 32 * i);
-            tmem_ld_wait<GR>(r);
+            for (int i = 0; i < COLS / 32; ++i) tmem_ld32(tl + C::TM_S0 + b * 128 + col0 + 32 * i, r + 32 * i);
+            tmem_ld_wait<COLS>(r);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(C::B_SFREE + b));
             // scores in base-2 units, and for each row the largest of what decides the weights' range
             float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-            const float* scales = reinterpret_cast<const float*>(smem + C::OFF_SCALE) + sc * 384 + group * GR;
+            const float* scales = reinterpret_cast<const float*>(smem + C::OFF_SCALE) + sc * 384 + col0;
             if constexpr (FP8) {
 #pragma unroll
-              for (int k = 0; k < GR; k += 4) {
+              for (int k = 0; k < COLS; k += 4) {
                 const float4 ks = *reinterpret_cast<const float4*>(scales + k);
                 const uint64_t a = fmul2(f2pack(__uint_as_float(r[k]), __uint_as_float(r[k + 1])), f2pack(rq, rq));
                 const uint64_t bb = fmul2(f2pack(__uint_as_float(r[k + 2]), __uint_as_float(r[k + 3])), f2pack(rq, rq));
@@ -683,15 +705,15 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
               }
             } else {
 #pragma unroll
-              for (int k = 0; k < GR; ++k) s[k] = __uint_as_float(r[k]);
+              for (int k = 0; k < COLS; ++k) s[k] = __uint_as_float(r[k]);
             }
             if (edge) {
 #pragma unroll
-              for (int k = 0; k < GR; ++k)
-                if (!((seen[k / 32] >> (k & 31)) & 1u)) s[k] = -INFINITY;
+              for (int k = 0; k < COLS; ++k)
+                if (!(((wg == 0 ? seen[k / 32] : seen[(COLS * (C::NW - 1) + k) / 32]) >> (k & 31)) & 1u)) s[k] = -INFINITY;
             }
 #pragma unroll
-            for (int k = 0; k < GR; k += 8) {
+            for (int k = 0; k < COLS; k += 8) {
               float v[8];
 #pragma unroll
               for (int e = 0; e < 8; ++e) v[e] = s[k + e];
@@ -707,6 +729,15 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
               for (int e = 0; e < 4; ++e) top[e] = fmax3(top[e], v[2 * e], v[2 * e + 1]);
             }
             float tile_top = fmaxf(fmax3(top[0], top[1], top[2]), top[3]);
+            if constexpr (C::NW == 2) {  // both halves' largest
+              float* tops = reinterpret_cast<float*>(smem + C::OFF_TOPS) + top_parity * 256;
+              tops[wg * 128 + row] = tile_top;
+              __syncwarp();
+              if (lane == 0) mbar_arrive(bar(C::B_TOP + wq));
+              if (!(ok = mbar_rest_warp(bar(C::B_TOP + wq), top_parity, guard, SITE_TREE_SOFTMAX))) break;
+              tile_top = fmaxf(tile_top, tops[(1 - wg) * 128 + row]);
+              top_parity ^= 1;
+            }
             if constexpr (!FP8) tile_top *= p.c_log2;
             constexpr float kStart = FP8 ? -kF16Start : kFwdMaxHeadroom, kMove = FP8 ? kF16Top : kFwdRescaleThreshold;
             if (j == 0) {
@@ -724,7 +755,7 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
                   break;
                 tc_fence_after();
 #pragma unroll 1
-                for (int i = 0; i < D / 32; ++i) {
+                for (int i = wg; i < D / 32; i += C::NW) {
                   uint32_t o[32];
                   tmem_ld32(tl + C::TM_O + 32 * i, o);
                   tmem_ld_wait<32>(o);
@@ -739,9 +770,9 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
             const uint64_t neg2 = f2pack(neg, neg), cc2 = f2pack(p.c_log2, p.c_log2);
             uint64_t ls[2] = {f2pack(0.f, 0.f), f2pack(0.f, 0.f)};
             float rl[2] = {0.f, 0.f}, rh[2] = {0.f, 0.f};
-            uint32_t pk[GR / 2];
+            uint32_t pk[COLS / 2];
 #pragma unroll
-            for (int k = 0; k < GR; k += 4) {
+            for (int k = 0; k < COLS; k += 4) {
               uint64_t vsc[2];
               if constexpr (FP8) {
                 const float4 a = *reinterpret_cast<const float4*>(scales + 128 + k);
@@ -773,19 +804,15 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
             // the product that read this P buffer is done
             if (!(ok = mbar_rest_warp(bar(C::B_PFREE + pb), pfree, guard, SITE_TREE_SOFTMAX))) break;
             tc_fence_after();
-            const uint32_t own = tl + C::TM_P0 + pb * 64 + group * (GR / 2);
-            if constexpr (NS == 4) tmem_st16(own, pk);
-            if constexpr (NS == 2) tmem_st32(own, pk);
-            if constexpr (NS == 1) {
-              tmem_st32(own, pk);
-              tmem_st32(own + 32, pk + 32);
-            }
+            const uint32_t own = tl + C::TM_P0 + pb * 64 + col0 / 2;
+            if constexpr (COLS == 32) tmem_st16(own, pk);
+            else tmem_st32(own, pk);
             tmem_st_wait();
           } else {
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(C::B_SFREE + b));
           }
-          if (k0 + kKeys > inside) {  // the tile holds drafted tokens or rows behind the end
+          if (lead && k0 + kKeys > inside) {  // the tile holds drafted tokens or rows behind the end
             if (!(ok = mbar_rest_warp(bar(C::B_FULL + vs_slot), vpar, guard, SITE_TREE_SOFTMAX)) || !(ok = meet())) break;
             // (a single token sees itself, or its row sees nothing at all: its values need no look)
             clean_values<D, FP8, NS>(sb + C::OFF_T + vs_slot * C::TILE, row, max(inside - k0, 0),
@@ -808,6 +835,20 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
           raw_len = c.lens[w.b], raw_new = new_of(w.b);
           table.open(c, w.b, w.t0 * kKeys, kKeys / boxes, lane);
           take_q(w);  // the next unit's S may be formed meanwhile
+        }
+        if constexpr (C::NW == 2) {
+          // the second warpgroup's sums, for the first; before the next ones it waits until these have been read
+          if (!lead) {
+            if (seg > 0 && !(ok = mbar_rest_warp(bar(C::B_OFREE), (seg - 1) & 1, guard, SITE_TREE_SOFTMAX))) break;
+            rows[128 + row] = l;
+            rows[256 + row] = lr;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(C::B_LSUM));
+            continue;
+          }
+          if (!(ok = mbar_rest_warp(bar(C::B_LSUM), seg & 1, guard, SITE_TREE_SOFTMAX))) break;
+          l += rows[128 + row];
+          lr += rows[256 + row];
         }
         if (!(ok = mbar_rest_warp(bar(C::B_OFULL), seg & 1, guard, SITE_TREE_SOFTMAX)) || !(ok = meet())) break;
         tc_fence_after();
@@ -960,13 +1001,12 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
       }
     }
   } else if constexpr (FP8) {
-    regs_dec<112>();
+    regs_dec<kConvertRegs>();
     if (!skip) {
       // ---------------------------------------------------------------- e4m3 -> f16 tiles
-      // Pairs of warps: 8, 9 and 12, 13 take the K tiles in turn, 10, 11 and 14, 15 the V tiles.  Four tiles are
-      // under way at once, as most of a tile's time is waits (its barriers, the fence): with two groups of four
-      // warps it took 2050 cycles.
-      const int kv = (warp >> 1) & 1, half = (warp - 8) >> 2, tid = threadIdx.x & 63;
+      // Pairs of warps take a tile each: K and V, and with two pairs for each of them every other one, so that four
+      // tiles are under way at once, as most of a tile's time is waits (its barriers, the fence).
+      const int cw = warp - 4 - 4 * C::NW, kv = (cw >> 1) & 1, half = cw >> 2, tid = threadIdx.x & 63;
       constexpr int PPR = D / 16, NP = 2 * PPR;  // 16-byte pieces of an e4m3 row; of a thread
       // Piece `sub` of rows k * ROWS + row, k < NP.  Eight lanes read 128 bytes of different banks and write 16-byte
       // units of different banks: at d = 128 (two chunks, 8 pieces a row) lanes 4..7 of eight take the upper half of
@@ -986,7 +1026,7 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
       for (; ok && w.more(); w.next(c, hms)) {
         const int n = w.n();
         int j = skip_tiles;
-        for (; j < n; j += 2) {
+        for (; j < n; j += C::NPAIR) {
           if (!(ok = mbar_rest_warp(bar(C::B_RFULL + rs), rpar, guard, SITE_TREE_CONVERT))) break;
           const uint32_t raw = sb + C::OFF_RAW + rs * C::RAW, dst = sb + C::OFF_T + s * C::TILE;
           uint4 x[NP];
@@ -1011,7 +1051,7 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
             scale[0] = make_float2(power(ek & 255), power(ek >> 8));
             scale[64] = make_float2(power(ev & 255), power(ev >> 8));
             scale[128] = make_float2(exponent(ev & 255), exponent(ev >> 8));
-            if ((sc += 2) >= C::NSC) sc -= C::NSC;
+            if ((sc += C::NPAIR) >= C::NSC) sc -= C::NSC;
           }
 #pragma unroll
           for (int k = 0; k < NP; ++k) {
@@ -1025,8 +1065,8 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(C::B_FULL + s));
-          if ((rs += 4) >= C::NRAW) rs -= C::NRAW, rpar ^= 1;
-          if ((s += 4) >= C::NSLOT) s -= C::NSLOT, spar ^= 1;
+          if ((rs += 2 * C::NPAIR) >= C::NRAW) rs -= C::NRAW, rpar ^= 1;
+          if ((s += 2 * C::NPAIR) >= C::NSLOT) s -= C::NSLOT, spar ^= 1;
         }
         if (!ok) break;
         skip_tiles = j - n;
