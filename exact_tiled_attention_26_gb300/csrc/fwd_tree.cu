@@ -103,7 +103,7 @@ struct TCfg {
   static constexpr int OFF_SCALE = OFF_RAW + NRAW * RAW;  // [NSC][3][128] floats: 2^k of K, 2^k of V, k of V
   static constexpr int OFF_ROWS = OFF_SCALE + NSC * 3 * 128 * 4;  // [3][128] floats
   static constexpr int OFF_TOPS = OFF_ROWS + 3 * 128 * 4;         // NW = 2: [2][2][128] floats
-  static constexpr int OFF_BAR = OFF_TOPS + (NW == 2 ? 2048 : 0);
+  static constexpr int OFF_BAR = OFF_TOPS + (NW == 2 ? 2560 : 0);  // (and [128] of Q's scales)
   static constexpr int B_QREADY = 0, B_FULL = 1, B_EMPTY = B_FULL + NSLOT,
                        B_RFULL = B_EMPTY + NSLOT, B_REMPTY = B_RFULL + NRAW, B_SFULL = B_REMPTY + NRAW,
                        B_SFREE = B_SFULL + NSB, B_PFULL = B_SFREE + NSB, B_PFREE = B_PFULL + NPB, B_OFULL = B_PFREE + NPB, B_OFREE = B_OFULL + 1,
@@ -119,8 +119,8 @@ struct TCfg {
   static constexpr int NTHREADS = FP8 ? 512 : 128 + 128 * NW;
   // setmaxnreg shares of issue, softmax and converting warps (0: none); their sums over the warpgroups stay within
   // the launch's: 4 x 128 with 512 threads, 3 x 168 with 384
-  static constexpr int R_ISSUE = FP8 ? (NW == 2 ? 64 : 80) : NW == 2 ? 64 : 0;
-  static constexpr int R_SOFT = FP8 ? (NW == 2 ? 168 : 208) : NW == 2 ? 216 : 0;
+  static constexpr int R_ISSUE = FP8 ? (NW == 2 ? 64 : 80) : 0;
+  static constexpr int R_SOFT = FP8 ? (NW == 2 ? 168 : 208) : 0;
   static_assert(SMEM <= 232448, "shared memory budget");
   static_assert(TM_Q + D / 2 <= TM_COLS, "tensor memory budget");
 };
@@ -587,7 +587,9 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
       // For an e4m3 cache the row becomes f16, scaled by a power of two to a maximum in [2^14, 2^15): elements
       // of 2^-31 of the maximum and more keep all their bits.
       float q_scale = 0.f;
+      [[maybe_unused]] float* q_scales = reinterpret_cast<float*>(smem + C::OFF_TOPS) + 512;
       auto take_q = [&](const Walk& at) {
+        if (!lead) return;
         const int h = p.M == 1 ? at.hm : at.hm / p.M, q = (at.hm - h * p.M) * 128 + r_in;
         uint4 x[D / 8];
         const uint4* src =
@@ -609,7 +611,7 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
           mul = __int_as_float((268 - e) << 23);                     // 2^(14 - (e - 127))
           q_scale = p.c_log2 * __int_as_float((e - 14) << 23);
         }
-        if (!lead) return;
+        if (C::NW == 2) q_scales[row] = q_scale;
 #pragma unroll
         for (int k = 0; k < D / 32; ++k) {
           uint32_t o[16];
@@ -654,6 +656,10 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
         const bool warp_live = mt * 128 + (wq * 32) % GR < p.R;
         const unsigned long long* trow =
             p.tree == nullptr ? nullptr : p.tree + w.b * p.tree_stride + static_cast<size_t>(t) * p.words;
+        if (!lead) {  // the scale of its row, from the first warpgroup
+          if (!(ok = mbar_rest_warp(bar(C::B_QREADY), seg & 1, guard, SITE_TREE_SOFTMAX))) break;
+          q_scale = q_scales[row];
+        }
         const float rq = q_scale;
         float ref = -INFINITY, l = 0.f, lr = 0.f;  // reference, sum of weights, sum of weights as rounded
         Poison<D> poison;
@@ -770,43 +776,48 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
             const uint64_t neg2 = f2pack(neg, neg), cc2 = f2pack(p.c_log2, p.c_log2);
             uint64_t ls[2] = {f2pack(0.f, 0.f), f2pack(0.f, 0.f)};
             float rl[2] = {0.f, 0.f}, rh[2] = {0.f, 0.f};
-            uint32_t pk[COLS / 2];
+            // 32 keys at a time: few registers
 #pragma unroll
-            for (int k = 0; k < COLS; k += 4) {
-              uint64_t vsc[2];
-              if constexpr (FP8) {
-                const float4 a = *reinterpret_cast<const float4*>(scales + 128 + k);
-                vsc[0] = f2pack(a.x, a.y), vsc[1] = f2pack(a.z, a.w);
-              }
+            for (int k0c = 0; k0c < COLS; k0c += 32) {
+              uint32_t pk[16];
 #pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const uint64_t x = f2pack(s[k + 2 * e], s[k + 2 * e + 1]);
-                float t0, t1;
-                f2unpack(FP8 ? fadd2(x, neg2) : ffma2(x, cc2, neg2), t0, t1);
-                const uint64_t w2 = f2pack(ex2(t0), ex2(t1));
-                ls[e] = fadd2(ls[e], w2);
-                float p0, p1;
+              for (int k = k0c; k < k0c + 32; k += 4) {
+                uint64_t vsc[2];
                 if constexpr (FP8) {
-                  f2unpack(fmul2(w2, vsc[e]), p0, p1);
-                  pk[k / 2 + e] = pack_f16x2(p0, p1);
-                } else {
-                  f2unpack(w2, p0, p1);
-                  pk[k / 2 + e] = pack_bf16x2(p0, p1);
-                  add_bf16x2_f32(pk[k / 2 + e], rl[e], rh[e]);
+                  const float4 a = *reinterpret_cast<const float4*>(scales + 128 + k);
+                  vsc[0] = f2pack(a.x, a.y), vsc[1] = f2pack(a.z, a.w);
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const uint64_t x = f2pack(s[k + 2 * e], s[k + 2 * e + 1]);
+                  float t0, t1;
+                  f2unpack(FP8 ? fadd2(x, neg2) : ffma2(x, cc2, neg2), t0, t1);
+                  const uint64_t w2 = f2pack(ex2(t0), ex2(t1));
+                  ls[e] = fadd2(ls[e], w2);
+                  const int at = (k - k0c) / 2 + e;
+                  float p0, p1;
+                  if constexpr (FP8) {
+                    f2unpack(fmul2(w2, vsc[e]), p0, p1);
+                    pk[at] = pack_f16x2(p0, p1);
+                  } else {
+                    f2unpack(w2, p0, p1);
+                    pk[at] = pack_bf16x2(p0, p1);
+                    add_bf16x2_f32(pk[at], rl[e], rh[e]);
+                  }
                 }
               }
+              if (k0c == 0) {  // the product that read this P buffer is done
+                if (!(ok = mbar_rest_warp(bar(C::B_PFREE + pb), pfree, guard, SITE_TREE_SOFTMAX))) break;
+                tc_fence_after();
+              }
+              tmem_st16(tl + C::TM_P0 + pb * 64 + (col0 + k0c) / 2, pk);
             }
+            if (!ok) break;
             float a0, a1;
             f2unpack(fadd2(ls[0], ls[1]), a0, a1);
             l += a0 + a1;
             // bf16 weights are normalised by their own sum; f16 ones are off by 2^-11 at most
             lr = FP8 ? l : lr + (rl[0] + rl[1]) + (rh[0] + rh[1]);
-            // the product that read this P buffer is done
-            if (!(ok = mbar_rest_warp(bar(C::B_PFREE + pb), pfree, guard, SITE_TREE_SOFTMAX))) break;
-            tc_fence_after();
-            const uint32_t own = tl + C::TM_P0 + pb * 64 + col0 / 2;
-            if constexpr (COLS == 32) tmem_st16(own, pk);
-            else tmem_st32(own, pk);
             tmem_st_wait();
           } else {
             __syncwarp();
