@@ -52,7 +52,7 @@ namespace {
 
 constexpr int kMaxGrid = 152;  // CTAs at most, one per SM
 constexpr int kKeys = 128;     // keys per tile
-constexpr int kUnitCost = 3;   // see Walk
+constexpr int kUnitCost = 6;   // see Walk
 constexpr int kConvertRegs = 112;
 
 enum : int { SITE_TREE_PRODUCER = 0x501, SITE_TREE_MMA = 0x502, SITE_TREE_SOFTMAX = 0x503, SITE_TREE_CONVERT = 0x504 };
@@ -140,6 +140,9 @@ FA_DEV long long quotient(long long a, long long b) {
 // A CTA's run.  The units stand one after the other on a line, each with kUnitCost places
 // (what starting and ending a unit costs, in tiles) before its tiles, and the CTAs take
 // equal runs of places: those with a unit's border in them get that many tiles less.
+// Measured for kUnitCost 0 / 3 / 5 / 8: 12 drafts x 8 sequences up to 8192, bf16 44.7 /
+// 38.0 / 36.6 / 36.1 us; 63 drafts x 4 sequences up to 16384, e4m3 104.7 / 95.1 / 91.1 /
+// 92.1; a single token over 1000 keys 9.1 / 9.3 / 9.4 / 9.3.
 struct Walk {
   int b, hm, t0, nt;  // sequence, key head and row tile (h * M + mt), first tile, tiles of the unit
   int cost;           // places before the first tile
@@ -1143,14 +1146,23 @@ __global__ void __launch_bounds__(128) tree_join_kernel(const __grid_constant__ 
         float v[8][E];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float* at = slot(k0 + min(i0 + i, cnt - 1)) + static_cast<size_t>(r) * D + lane * E;
-#pragma unroll
-          for (int e = 0; e < E; ++e) v[i][e] = at[e];
+          if (i0 + i >= cnt) break;
+          const float* at = slot(k0 + i0 + i) + static_cast<size_t>(r) * D + lane * E;
+          if constexpr (E == 4) {
+            const float4 x = *reinterpret_cast<const float4*>(at);
+            v[i][0] = x.x, v[i][1] = x.y, v[i][2] = x.z, v[i][3] = x.w;
+          } else if constexpr (E == 2) {
+            const float2 x = *reinterpret_cast<const float2*>(at);
+            v[i][0] = x.x, v[i][1] = x.y;
+          } else {
+            v[i][0] = at[0];
+          }
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const float fi = __shfl_sync(0xffffffffu, f, (i0 + i) & 31);
-          if (i0 + i < cnt && fi != 0.f) {
+          if (i0 + i >= cnt) break;
+          if (fi != 0.f) {
 #pragma unroll
             for (int e = 0; e < E; ++e) o[e] = fmaf(fi, v[i][e], o[e]);
           }
