@@ -96,7 +96,7 @@ struct TCfg {
   static constexpr int RAW = 128 * D + 256;     // with the exponent bytes of its keys (K tiles: and of their values)
   static constexpr int NSB = 2;                 // S buffers in tensor memory
   static constexpr int NPB = D == 128 ? 1 : 2;  // P buffers
-  static constexpr int NSC = FP8 ? NSLOT / 2 + NSB : 0;  // tiles whose scales are kept (see the converter)
+  static constexpr int NSC = FP8 ? NSLOT / 2 + NSB + 1 : 0;  // tiles whose scales are kept (see the converter)
   static constexpr int OFF_T = 0;
   static constexpr int OFF_X = OFF_T + NSLOT * TILE;      // the epilogue's exchange
   static constexpr int OFF_RAW = OFF_X + (NS > 1 ? 16384 : 0);
@@ -1055,9 +1055,9 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
           if (lane == 0) mbar_arrive(bar(C::B_REMPTY + rs));  // the next tile may come while this one is converted
           if (!(ok = mbar_rest_warp(bar(C::B_EMPTY + s), spar, guard, SITE_TREE_CONVERT))) break;
           if (kv == 0) {
-            // The tile's scales, for the softmax warps.  This slot held the K tile NSLOT / 2 tiles ago, whose S is
-            // done; so the P of NSB tiles before that was used, and the softmax is past it: the NSLOT / 2 + NSB - 1
-            // tiles it may still read are not overwritten.
+            // The tile's scales, for the softmax warps.  This slot held K tile x - NSLOT / 2, whose S is done; so it was
+            // begun, and the scores of tile x - NSLOT / 2 - NSB had been taken out of its S buffer.  That tile's weights
+            // may still be in the making: it and the NSLOT / 2 + NSB - 1 tiles behind it are not overwritten.
             float2* scale = reinterpret_cast<float2*>(smem + C::OFF_SCALE + sc * 1536) + tid;
             // (a row that holds NaN has NaN elements: its scale is 1)
             auto power = [](int e) { return e == kExpNaN ? 1.f : __int_as_float(e << 23); };

@@ -227,6 +227,40 @@ def test_large_scores_and_a_long_ragged_batch(fa_lib):
             assert abs(float(lse[b, h, 0]) - L) <= e + 2.0 ** -18 * (1 + abs(L))
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("d, G, T", [(128, 4, 1), (128, 5, 12), (128, 4, 63), (64, 1, 24), (64, 8, 9), (32, 3, 33)])
+def test_long_caches_again_and_again(fa_lib, fp8, d, G, T):
+    """Sequences long enough to run every ring round many times, each call the same bits, and right against fp64."""
+    fa = fa_lib
+    B, Hk, page, cols = 3, 8, 64, 150
+    q, cache, table, g = make(fa, B, Hk * G, Hk, T, d, page, cols, fp8, 16 + d + T)
+    lens = torch.tensor([9600, 5001, 7300], dtype=torch.int32)
+    put(fa, cache, table, lens, g)
+    words, bits = random_tree(B, T, g)
+    args = (q.to(DEV), cache, table.to(DEV), lens.to(DEV), words.to(DEV))
+    o, lse = fa.attention_tree(*args)
+    for _ in range(30):
+        again = fa.attention_tree(*args)
+        assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
+    k, v = fa.cache_read(cache, table.to(DEV), lens.to(DEV), cols * page)
+    for b in range(B):
+        n = int(lens[b])
+        see = torch.ones(T, n, dtype=torch.bool)
+        see[:, n - T:] = torch.tensor([[bool(bits[b][t] >> j & 1) for j in range(T)] for t in range(T)])
+        see = see.to(DEV).repeat(G, 1)
+        for hk in range(Hk):
+            kk, vv = k[b, hk, :n].double(), v[b, hk, :n].double()
+            rows = args[0][b, hk * G:(hk + 1) * G].reshape(G * T, d).double()
+            s = (rows @ kk.T / math.sqrt(d)).masked_fill(~see, -math.inf)
+            e = 2 * d * 2.0 ** -24 * (rows.abs() @ kk.abs().T).amax(-1, keepdim=True) / math.sqrt(d)
+            w = torch.softmax(s, -1)
+            ref, mag = w @ vv, w @ vv.abs()
+            got = o[b, hk * G:(hk + 1) * G].reshape(G * T, d).double()
+            assert ((got - ref).abs() <= 2.0 ** -8 * ref.abs() + (2.0 ** -7 + 2 * e + 2.0 ** -14) * mag).all(), (b, hk)
+            L = torch.logsumexp(s, -1)
+            assert ((lse[b, hk * G:(hk + 1) * G].reshape(-1).double() - L).abs() <= e[:, 0] + 2.0 ** -18 * (1 + L.abs())).all()
+
+
 def test_guard_bands_and_a_dirty_workspace(fa_lib):
     fa = fa_lib
     B, H, Hk, T, d, page, cols = 3, 4, 2, 5, 64, 16, 30
