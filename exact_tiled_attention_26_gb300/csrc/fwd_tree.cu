@@ -825,6 +825,8 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
           } else {
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(C::B_SFREE + b));
+            // no rows, no weights; but without this wait its arrival below could count for an earlier tile's
+            if (!(ok = mbar_rest_warp(bar(C::B_PFREE + pb), pfree, guard, SITE_TREE_SOFTMAX))) break;
           }
           if (lead && k0 + kKeys > inside) {  // the tile holds drafted tokens or rows behind the end
             if (!(ok = mbar_rest_warp(bar(C::B_FULL + vs_slot), vpar, guard, SITE_TREE_SOFTMAX)) || !(ok = meet())) break;
