@@ -54,7 +54,7 @@ def _load():
 lib = _load()
 
 _vp, _i, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
-_ll, _strides = ctypes.c_longlong, ctypes.POINTER(ctypes.c_longlong)
+_ll, _strides = ctypes.c_longlong, ctypes.c_void_p  # strides: the address of three long longs, or None
 
 FA_CACHE_BF16, FA_CACHE_E4M3 = range(2)
 

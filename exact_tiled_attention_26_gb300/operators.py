@@ -12,7 +12,7 @@ import math
 
 import torch
 
-from . import FA_CACHE_BF16, FA_CACHE_E4M3, FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED, _ll3, check, fa_cache, lib
+from . import FA_CACHE_BF16, FA_CACHE_E4M3, FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED, check, fa_cache, lib
 
 _BF16, _F32, _I32, _I64, _U8, _E4M3 = (torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.uint8,
                                        torch.float8_e4m3fn)
@@ -32,6 +32,10 @@ def _call(fn, what, device, *args):
         check(status, what)
 
 
+_Longs6, _Longs18 = ctypes.c_longlong * 6, ctypes.c_longlong * 18
+_address = ctypes.addressof
+
+
 def _ptr(t):
     """Address of a tensor's elements; None for no tensor and for an empty one."""
     return None if t is None else t.data_ptr() or None
@@ -44,7 +48,7 @@ def _check_rows(name, t):
     st = t.stride()
     if st[3] != 1 and t.numel() and t.shape[3] > 1:
         raise ValueError(f"{name}: the elements of a row must be contiguous")
-    return None if t.is_contiguous() else st[:3]
+    return st[:3]
 
 
 def _check_ints(name, t, shape, device):
@@ -94,8 +98,9 @@ def qk_norm_rope(q, k, q_weight=None, k_weight=None, cos=None, sin=None, positio
     Hk = k.shape[1]
     qo = torch.empty((B, H, N, d), dtype=_BF16, device=q.device)
     ko = torch.empty((B, Hk, N, d), dtype=_BF16, device=q.device)
-    _call(lib.fa_qk_norm_rope, "fa_qk_norm_rope", device, _ptr(q), _ptr(k), _ptr(qo), _ptr(ko), _ll3(sq), _ll3(sk),
-          _ptr(q_weight), _ptr(k_weight), bf16, _ptr(cos), _ptr(sin), rope, rows, 1 if interleaved else 0,
+    strides = _Longs6(*sq, *sk)
+    at = _address(strides)
+    _call(lib.fa_qk_norm_rope, "fa_qk_norm_rope", device, _ptr(q), _ptr(k), _ptr(qo), _ptr(ko), at, at + 24, _ptr(q_weight), _ptr(k_weight), bf16, _ptr(cos), _ptr(sin), rope, rows, 1 if interleaved else 0,
           _ptr(positions), B, H, Hk, N, d, eps)
     return qo, ko
 
@@ -122,15 +127,12 @@ def qk_norm_rope_backward(q, k, dq_out, dk_out, q_weight=None, k_weight=None, co
         workspace, n = _workspace(workspace, need, q.device)
     else:
         workspace = None
+    strides = _Longs18(*sq, *sk, *sdq, *sdk, *dq.stride()[:3], *dk.stride()[:3])
+    at = _address(strides)
     _call(lib.fa_qk_norm_rope_bwd, "fa_qk_norm_rope_bwd", device, _ptr(q), _ptr(k), _ptr(dq_out), _ptr(dk_out), _ptr(dq),
-          _ptr(dk), _ll3(sq), _ll3(sk), _ll3(sdq), _ll3(sdk), _ll3(_layout(dq)), _ll3(_layout(dk)), _ptr(q_weight),
-          _ptr(k_weight), _ptr(dqw), _ptr(dkw), bf16, _ptr(cos), _ptr(sin), rope, rows, 1 if interleaved else 0,
+          _ptr(dk), at, at + 24, at + 48, at + 72, at + 96, at + 120, _ptr(q_weight), _ptr(k_weight), _ptr(dqw), _ptr(dkw), bf16, _ptr(cos), _ptr(sin), rope, rows, 1 if interleaved else 0,
           _ptr(positions), B, H, Hk, N, d, eps, _ptr(workspace), n)
     return dq, dk, dqw, dkw
-
-
-def _layout(t):
-    return None if t.is_contiguous() else t.stride()[:3]
 
 
 def _workspace(workspace, need, device):
@@ -219,7 +221,9 @@ def cache_write(cache, k, v, table, lens, n_new=None):
     if v.shape != k.shape or v.get_device() != device or B != table.shape[0] or hk != c.Hk or d != c.d or \
             device != cache.k.get_device():
         raise ValueError("k and v must be [B, Hk, T, d] with the table's B and the cache's Hk and d, on its device")
-    _call(lib.fa_cache_write, "fa_cache_write", device, c, _ptr(k), _ptr(v), _ll3(sk), _ll3(sv), B, T, *tab, _ptr(n_new))
+    strides = _Longs6(*sk, *sv)
+    at = _address(strides)
+    _call(lib.fa_cache_write, "fa_cache_write", device, c, _ptr(k), _ptr(v), at, at + 24, B, T, *tab, _ptr(n_new))
 
 
 def cache_read(cache, table, lens, length):
