@@ -1062,8 +1062,10 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
             // may still be in the making: it and the NSLOT / 2 + NSB - 1 tiles behind it are not overwritten.
             float2* scale = reinterpret_cast<float2*>(smem + C::OFF_SCALE + sc * 1536) + tid;
             // (a row that holds NaN has NaN elements: its scale is 1)
-            auto power = [](int e) { return e == kExpNaN ? 1.f : __int_as_float(e << 23); };
-            auto exponent = [](int e) { return e == kExpNaN ? 0.f : static_cast<float>(e - 127); };
+            // (bytes below kExpMin are of rows never written, a fresh cache's zeros: with an exponent below -100
+            // their unscaled weights would pass fp32's range)
+            auto power = [](int e) { return e == kExpNaN ? 1.f : __int_as_float(max(e, kExpMin) << 23); };
+            auto exponent = [](int e) { return e == kExpNaN ? 0.f : static_cast<float>(max(e, kExpMin) - 127); };
             scale[0] = make_float2(power(ek & 255), power(ek >> 8));
             scale[64] = make_float2(power(ev & 255), power(ev >> 8));
             scale[128] = make_float2(exponent(ev & 255), exponent(ev >> 8));

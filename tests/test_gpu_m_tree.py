@@ -332,3 +332,113 @@ def test_refusals_of_the_helper(fa_lib):
             bad()
     with pytest.raises(fa.FAError):
         fa.attention_tree(q, c, t, n, scale=-1.0)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_pages_past_32_bit_offsets(fa_lib, fp8):
+    """A cache of more than 2^32 bytes and elements: rows written, read and attended to at its far end."""
+    fa = fa_lib
+    Hk, page, d = 4, 128, 128
+    pages = 2 ** 32 // (Hk * page * d) + 40
+    cache = fa.new_cache(pages, Hk, page, d, E4M3 if fp8 else torch.bfloat16)
+    assert cache.k.numel() > 2 ** 32
+    g = torch.Generator().manual_seed(31)
+    table = torch.tensor([[pages - 1, 3, pages - 2], [pages // 2 + 1, pages - 7, 0]], dtype=torch.int32)
+    lens = torch.tensor([300, 384], dtype=torch.int32)
+    k, v = (torch.randn(2, Hk, 384, d, generator=g).to(torch.bfloat16).to(DEV) for _ in range(2))
+    k, v = k[:, :, :300].contiguous(), v[:, :, :300].contiguous()
+    fa.cache_write(cache, k, v, table.to(DEV), torch.tensor([300, 384], dtype=torch.int32, device=DEV))
+    rk, rv = fa.cache_read(cache, table.to(DEV), lens.to(DEV), 384)
+    if not fp8:
+        assert torch.equal(rk[0, :, :300], k[0]) and torch.equal(rv[1, :, 84:], v[1])
+    assert not rk[0, :, 300:].any() and not rv[1, :, :84].any()
+    q = torch.randn(2, 8, 2, d, generator=g).to(torch.bfloat16).to(DEV)
+    o, lse = fa.attention_tree(q, cache, table.to(DEV), lens.to(DEV))
+    for b in range(2):
+        n = int(lens[b])
+        for h in range(8):
+            for t in range(2):
+                see = slice(0, n - 1 + t)
+                kk, vv = rk[b, h // 2, see].double(), rv[b, h // 2, see].double()
+                prod = q[b, h, t].double() * kk
+                s = prod.sum(-1) / math.sqrt(d)
+                e = 2 * d * 2.0 ** -24 * float(prod.abs().sum(-1).max()) / math.sqrt(d)
+                w = torch.softmax(s, 0)
+                ref, mag = w @ vv, w @ vv.abs()
+                assert ((o[b, h, t].double() - ref).abs() <= 2.0 ** -8 * ref.abs() + (2.0 ** -7 + 2 * e + 2.0 ** -14) * mag).all()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_many_sequences_of_few_keys(fa_lib, fp8):
+    """More sequences than a warp has lanes, many more units than CTAs, lengths 0 to 40, against the oracle at some."""
+    fa = fa_lib
+    B, H, Hk, d, page, cols = 700, 4, 2, 64, 16, 3
+    q, cache, table, g = make(fa, B, H, Hk, 1, d, page, cols, fp8, 41)
+    lens = torch.randint(0, 41, (B,), generator=g, dtype=torch.int32)
+    put(fa, cache, table, lens, g)
+    o, lse = fa.attention_tree(q.to(DEV), cache, table.to(DEV), lens.to(DEV))
+    assert torch.equal(torch.isneginf(lse).all(-1).all(-1).cpu(), lens == 0)
+    some = torch.arange(0, B, 9)
+    compare(o[some], lse[some], q[some], cache, table[some], lens[some], None, None, 1 / math.sqrt(d))
+
+
+def test_a_long_chunk_over_the_cache(fa_lib):
+    """300 new tokens for each of 4 heads of a key head (10 row tiles): the causal attention of the same tensors."""
+    fa = fa_lib
+    B, H, Hk, T, d, page, cols = 1, 4, 1, 300, 128, 64, 16
+    q, cache, table, g = make(fa, B, H, Hk, T, d, page, cols, False, 51)
+    lens = torch.tensor([900], dtype=torch.int32)
+    put(fa, cache, table, lens, g)
+    o, lse = fa.attention_tree(q.to(DEV), cache, table.to(DEV), lens.to(DEV))
+    k, v = fa.cache_read(cache, table.to(DEV), lens.to(DEV), 900)
+    ro, rl = fa.attention_forward(q.to(DEV), k.expand(B, H, 900, d).contiguous(), v.expand(B, H, 900, d).contiguous(), True)
+    # both round their weights and results to bf16 against the same exact value: twice the bound above, |v| < 5
+    assert (o.float() - ro.float()).abs().max() <= 2 * (2.0 ** -8 + 2.0 ** -7 + 2.0 ** -13) * 5
+    assert (lse - rl).abs().max() <= 2.0 ** -14
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_rows_never_written(fa_lib, fp8):
+    """A fresh cache reads as zeros: every key weighs the same and every value is zero."""
+    fa = fa_lib
+    cache = fa.new_cache(4, 2, 64, 128, E4M3 if fp8 else torch.bfloat16)
+    table = torch.arange(4, dtype=torch.int32, device=DEV).view(2, 2)
+    n = torch.tensor([128, 77], dtype=torch.int32, device=DEV)
+    q = torch.randn(2, 4, 1, 128, device=DEV).to(torch.bfloat16)
+    o, lse = fa.attention_tree(q, cache, table, n)
+    assert not o.any()
+    assert (lse - n.float().log()[:, None, None]).abs().max() <= 2.0 ** -18 * 6
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("G, T", [(1, 1), (8, 6), (8, 11)])
+def test_values_of_very_different_scales(fa_lib, fp8, G, T):
+    """Keys and values whose rows differ by up to 2^120 in size, zeros among them; query rows too."""
+    fa = fa_lib
+    B, Hk, d, page, cols = 2, 2, 64, 16, 40
+    q, cache, table, g = make(fa, B, Hk * G, Hk, T, d, page, cols, fp8, 61 + T)
+    lens = torch.tensor([640, 333], dtype=torch.int32)
+    n = cols * page
+    k = torch.randn(B, Hk, n, d, generator=g)
+    v = torch.randn(B, Hk, n, d, generator=g) * 2.0 ** torch.randint(-60, 61, (B, Hk, n, 1), generator=g)
+    v[:, :, ::7] = 0
+    k = k * 2.0 ** torch.randint(-20, 1, (B, Hk, n, 1), generator=g)
+    q = (q.float() * 2.0 ** torch.randint(-12, 3, (B, Hk * G, T, 1), generator=g)).to(torch.bfloat16)
+    full = torch.full((B,), n, dtype=torch.int32, device=DEV)
+    fa.cache_write(cache, k.to(torch.bfloat16).to(DEV), v.to(torch.bfloat16).to(DEV), table.to(DEV), full)
+    o, lse = fa.attention_tree(q.to(DEV), cache, table.to(DEV), lens.to(DEV))
+    compare(o, lse, q, cache, table, lens, None, None, 1 / math.sqrt(d))
+
+
+def test_no_pages_and_no_columns(fa_lib):
+    fa = fa_lib
+    q = torch.randn(2, 4, 3, 64, device=DEV).to(torch.bfloat16)
+    n = torch.tensor([5, 0], dtype=torch.int32, device=DEV)
+    x = torch.randn(2, 2, 3, 64, device=DEV).to(torch.bfloat16)
+    for cache, table in ((fa.new_cache(0, 2, 16, 64), torch.zeros(2, 3, dtype=torch.int32, device=DEV)),
+                         (fa.new_cache(4, 2, 16, 64), torch.zeros(2, 0, dtype=torch.int32, device=DEV))):
+        fa.cache_write(cache, x, x, table, n)
+        o, lse = fa.attention_tree(q, cache, table, n)
+        assert not o.any() and torch.isneginf(lse).all()
+        k, v = fa.cache_read(cache, table, n, 7)
+        assert k.shape == (2, 2, 7, 64) and not k.any() and not v.any()
