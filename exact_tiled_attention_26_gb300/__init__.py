@@ -383,7 +383,7 @@ def attention_fwd_bwd_host(q, k, v, do, causal=False, scale=None, window=0, head
 # KVCache, new_cache, qk_norm_rope, qk_norm_rope_backward, cache_write, cache_read, attention_tree and tree_words live
 # in operators.py, which imports PyTorch: loaded on first use, so that the binding itself does not need it.
 _OPERATORS = ("KVCache", "new_cache", "qk_norm_rope", "qk_norm_rope_backward", "cache_write", "cache_read",
-              "attention_tree", "tree_words", "_cache_args")
+              "attention_tree", "tree_words")
 
 
 def __getattr__(name):

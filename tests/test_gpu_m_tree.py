@@ -273,7 +273,7 @@ def test_guard_bands_and_a_dirty_workspace(fa_lib):
     bufs = [torch.full((n + 512,), 0xA5, dtype=torch.uint8, device=DEV) for n in sizes]
     bufs[2][256:256 + n_ws] = 0xFF
     qd, td, ld = q.to(DEV), table.to(DEV), lens.to(DEV)
-    c, _ = fa._cache_args(cache, td, ld, None)
+    c = fa.fa_cache(cache.k.data_ptr(), cache.v.data_ptr(), None, None, fa.FA_CACHE_BF16, *cache.k.shape)
     for _ in range(2):  # the second call on what the first left
         st = fa.fa_fwd_tree(qd.data_ptr(), c, bufs[0].data_ptr() + 256, bufs[1].data_ptr() + 256, B, H, T, td.data_ptr(),
                             cols, cols, ld.data_ptr(), None, None, 0, 1 / math.sqrt(d), bufs[2].data_ptr() + 256, n_ws,

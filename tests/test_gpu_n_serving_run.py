@@ -126,3 +126,37 @@ def test_the_oracle_agrees_with_the_cache_it_reads(fa_lib):
     rows, there = orc.sequence(cache.k.cpu().double(), table, 40, 16, 0)
     assert there.tolist() == [True] * 16 + [False] * 16 + [True] * 8
     assert torch.equal(rows[0, there], x[0, 0, there].double())
+
+
+def test_calls_keep_no_tensor(fa_lib):
+    """Returned and refused calls hold no reference to their tensors: after many calls the memory is what it was."""
+    import sys
+    fa = fa_lib
+    q = torch.randn(2, 4, 3, 64, device=DEV).to(torch.bfloat16)
+    k = torch.randn(2, 2, 3, 64, device=DEV).to(torch.bfloat16)
+    w = torch.ones(64, device=DEV)
+    cache = fa.new_cache(4, 2, 16, 64)
+    table = torch.tensor([[0], [1]], dtype=torch.int32, device=DEV)
+    lens = torch.tensor([3, 9], dtype=torch.int32, device=DEV)
+
+    def calls():
+        fa.cache_write(cache, k, k, table, lens)
+        fa.cache_read(cache, table, lens, 9)
+        fa.attention_tree(q, cache, table, lens)
+        fa.qk_norm_rope(q, k, w, w)
+        fa.qk_norm_rope_backward(q, k, q, k, w, w)
+        fa.qk_norm_rope_backward(q, k, q, k)
+        with pytest.raises(ValueError):
+            fa.attention_tree(q.float(), cache, table, lens)
+        with pytest.raises(fa.FAError):
+            fa.attention_tree(q, cache, table, lens, scale=-1.0)
+
+    calls()
+    torch.cuda.synchronize()
+    held = (q, k, w, cache.k, cache.v, table, lens)
+    before = torch.cuda.memory_allocated(), [sys.getrefcount(t) for t in held], sys.getrefcount(None)
+    for _ in range(200):
+        calls()
+    torch.cuda.synchronize()
+    after = torch.cuda.memory_allocated(), [sys.getrefcount(t) for t in held], sys.getrefcount(None)
+    assert after[:2] == before[:2] and abs(after[2] - before[2]) < 100

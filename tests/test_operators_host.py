@@ -159,6 +159,17 @@ def test_helpers_refuse_cpu_tensors(fa_lib):
         fa.new_cache(1, 1, 16, 64, dtype=torch.float16, device="cpu")
 
 
+def test_helpers_refuse_what_is_no_tensor(fa_lib):
+    fa = fa_lib
+    x = torch.zeros(1, 2, 3, 64, dtype=torch.bfloat16)
+    i = torch.zeros(1, 1, dtype=torch.int32)
+    for bad in (lambda: fa.qk_norm_rope(x, None), lambda: fa.qk_norm_rope([1.0], x), lambda: fa.qk_norm_rope(x, x, 1.0),
+                lambda: fa.cache_write(fa.KVCache(None, x), x, x, i, i[0]),
+                lambda: fa.attention_tree(7, fa.KVCache(x, x), i, i[0])):
+        with pytest.raises((TypeError, ValueError)):
+            bad()
+
+
 def test_tree_words(fa_lib):
     fa = fa_lib
     w = fa.tree_words([-1, 0, 0, 1, -1])
