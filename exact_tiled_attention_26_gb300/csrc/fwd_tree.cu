@@ -472,30 +472,24 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
             }
             __syncwarp();
             if (lane == 0) mbar_expect_tx(full, 128 * D + (kv == 0 ? 2 * n_there * rb : 0));
-            for (int i = 0; i < boxes; ++i) {
-              const int zi = __shfl_sync(0xffffffffu, z, i);
-              if (lane == 0) {
-                tma_load_3d(dst + i * rb * D, map, full, 0, y, zi);
-                if (kv == 0 && zi != nowhere) {
-                  const size_t at = static_cast<size_t>(zi) * c.page + y;
-                  bulk_load(dst + 128 * D + i * rb, c.Ke + at, rb, full);
-                  bulk_load(dst + 128 * D + 128 + i * rb, c.Ve + at, rb, full);
-                }
+            const unsigned long long at = static_cast<unsigned long long>(z) * c.page + y;
+            // Each lane issues its own box.  With lane 0 issuing all of them in turn the loads of K and the exponents
+            // bound the kernel: 128 us where this takes 114 (16 sequences up to 32768, e4m3), 89 where 83 (63 drafts).
+            __syncwarp();
+            if (issues) {
+              tma_load_3d(dst + lane * rb * D, map, full, 0, y, z);
+              if (kv == 0 && there) {
+                bulk_load(dst + 128 * D + lane * rb, c.Ke + at, rb, full);
+                bulk_load(dst + 128 * D + 128 + lane * rb, c.Ve + at, rb, full);
               }
             }
           } else {
             if (lane == 0) mbar_expect_tx(full, C::TILE);
-            int zs[8];
+            __syncwarp();
+            if (issues) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) zs[i] = __shfl_sync(0xffffffffu, z, i);
-            if (lane == 0) {
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                if (i >= boxes) break;
-#pragma unroll
-                for (int ch = 0; ch < D / C::CE; ++ch)
-                  tma_load_3d(dst + ch * 128 * C::SWB + i * rb * C::SWB, map, full, ch * C::CE, y, zs[i]);
-              }
+              for (int ch = 0; ch < D / C::CE; ++ch)
+                tma_load_3d(dst + ch * 128 * C::SWB + lane * rb * C::SWB, map, full, ch * C::CE, y, z);
             }
           }
           ++items;
