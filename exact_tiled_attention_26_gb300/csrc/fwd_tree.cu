@@ -38,16 +38,14 @@
 // largest of score + exponent of the value.
 //
 // Measured (d = 128, 8 key heads, 32 query heads, pages read once, device time):
-//   16 sequences up to 32768, a token each, e4m3: 121 to 129 us, 4.1 to 4.4 TB/s (61 to 64 % of a
-//     plain copy's rate).  A CTA takes some 2000 cycles a tile where its bytes take 1400: the chain
-//     load - convert - S - softmax - P V has five hand-overs a tile, and converting 32 KB
-//     takes the 8 warps most of a tile's time.  f16 tiles straight from a bf16 cache run at
-//     4.1 TB/s with 12 drafts x 8 sequences up to 8192 (36.8 us: short runs, of which
-//     starting, unit borders and the join are 10 us).
-//   63 drafts x 4 sequences up to 16384, e4m3: 90 us.  Bound by the softmax's instructions:
-//     every row weighs every key, 6.7e7 exponentials, scaled and packed; then the join of
-//     252-row units, 10 us.
-//   one token over 1000 keys: 9.3 us, two launches and one pass of latencies.
+//   16 sequences up to 32768, a token each, e4m3: 114 us, 4.6 TB/s (0.68 of a plain copy's rate).  A CTA takes some
+//     1750 cycles a tile where its bytes take 1400: the chain load - convert - S - softmax - P V has five hand-overs a
+//     tile, and the warp that loads K is busy issuing for most of it.
+//   12 drafts x 8 sequences up to 8192, bf16: 36.6 us, 4.1 TB/s; short runs, of which start, unit borders and the join
+//     are 10 us.
+//   63 drafts x 4 sequences up to 16384, e4m3: 83 us.  Bound by the softmax: every row weighs every key, 6.7e7
+//     exponentials, scaled and packed; then the join of 252-row units, 10 us.
+//   one token over 1000 keys: 9.1 us, two launches and one pass of latencies.
 //
 // Keys that are not there (behind the end, in no page) are masked; their values are
 // replaced by zeros before the product, as 0 * NaN would reach every row.  An infinite or
