@@ -42,7 +42,7 @@ def _calls_cmd(nvcc):
     torch = os.path.dirname(importlib.util.find_spec("torch").origin)
     includes = [os.path.join(ROOT, "include"), os.path.join(torch, "include"),
                 os.path.join(torch, "include", "torch", "csrc", "api", "include"), sysconfig.get_paths()["include"],
-                os.path.join(os.path.dirname(os.path.dirname(nvcc)), "include")]
+                os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include")]
     obj = os.path.join(BUILD, "tensor_calls.o")
     compile_ = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
                 f'-DFA_PACKAGE="{os.path.basename(PKG)}"', *[a for d in includes for a in ("-isystem", d)],

@@ -38,12 +38,12 @@
 // largest of score + exponent of the value.
 //
 // Measured (d = 128, 8 key heads, 32 query heads, pages read once, device time):
-//   16 sequences up to 32768, a token each, e4m3: 114 us, 4.6 TB/s (0.68 of a plain copy's rate).  A CTA takes some
-//     1750 cycles a tile where its bytes take 1400: the chain load - convert - S - softmax - P V has five hand-overs a
+//   16 sequences up to 32768, a token each, e4m3: 110 us, 4.8 TB/s (0.70 of a plain copy's rate).  A CTA takes some
+//     1700 cycles a tile where its bytes take 1400: the chain load - convert - S - softmax - P V has five hand-overs a
 //     tile, and the warp that loads K is busy issuing for most of it.
 //   12 drafts x 8 sequences up to 8192, bf16: 36.6 us, 4.1 TB/s; short runs, of which start, unit borders and the join
 //     are 10 us.
-//   63 drafts x 4 sequences up to 16384, e4m3: 83 us.  Bound by the softmax: every row weighs every key, 6.7e7
+//   63 drafts x 4 sequences up to 16384, e4m3: 78 us.  Bound by the softmax: every row weighs every key, 6.7e7
 //     exponentials, scaled and packed; then the join of 252-row units, 10 us.
 //   one token over 1000 keys: 9.1 us, two launches and one pass of latencies.
 //
@@ -1030,7 +1030,10 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
       // tiles are under way at once, as most of a tile's time is waits (its barriers, the fence).
       const int cw = warp - 4 - 4 * C::NW, kv = (cw >> 1) & 1, half = cw >> 2, tid = threadIdx.x & 63;
       constexpr int PPR = D / 16, NP = 2 * PPR;  // 16-byte pieces of an e4m3 row; of a thread
-      // Piece `sub` of rows k * ROWS + row, k < NP.  Eight lanes read 128 bytes of different banks and write 16-byte
+      // A loop of a few parts, as short code and few registers count for more than releasing the e4m3 tile early:
+      // 1 / 2 / 4 parts, 16 sequences of a token each 114 / 110 / 113 us, 63 drafts (one pair of warps) 83 / 80 / 78.
+      constexpr int PARTS = C::NPAIR == 1 ? 4 : 2, STEPS = NP / PARTS;
+      // Piece `sub` of rows (i * STEPS + k) * ROWS + row.  Eight lanes read 128 bytes of different banks and write 16-byte
       // units of different banks: at d = 128 (two chunks, 8 pieces a row) lanes 4..7 of eight take the upper half of
       // the neighbouring row, whose swizzle differs in the lowest bit.
       constexpr int ROWS = 64 / PPR;
@@ -1051,16 +1054,11 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
         for (; j < n; j += C::NPAIR) {
           if (!(ok = mbar_rest_warp(bar(C::B_RFULL + rs), rpar, guard, SITE_TREE_CONVERT))) break;
           const uint32_t raw = sb + C::OFF_RAW + rs * C::RAW, dst = sb + C::OFF_T + s * C::TILE;
-          uint4 x[NP];
-#pragma unroll
-          for (int k = 0; k < NP; ++k) x[k] = ld_shared_v4(raw + (k * ROWS + row) * D + sub * 16);
           int ek = 0, ev = 0;
           if (kv == 0) {
             const uint16_t* exps = reinterpret_cast<const uint16_t*>(smem + C::OFF_RAW + rs * C::RAW + 128 * D);
             ek = exps[tid], ev = exps[64 + tid];  // two keys' each
           }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(C::B_REMPTY + rs));  // the next tile may come while this one is converted
           if (!(ok = mbar_rest_warp(bar(C::B_EMPTY + s), spar, guard, SITE_TREE_CONVERT))) break;
           if (kv == 0) {
             // The tile's scales, for the softmax warps.  This slot held K tile x - NSLOT / 2, whose S is done; so it was
@@ -1077,14 +1075,25 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
             scale[128] = make_float2(exponent(ev & 255), exponent(ev >> 8));
             if ((sc += C::NPAIR) >= C::NSC) sc -= C::NSC;
           }
+#pragma unroll 1
+          for (int i = 0; i < PARTS; ++i) {
+            const uint32_t from = raw + (i * STEPS * ROWS + row) * D + sub * 16, part = dst + i * STEPS * ROWS * C::SWB;
+            uint4 x[STEPS];
 #pragma unroll
-          for (int k = 0; k < NP; ++k) {
-            const uint32_t w4[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-            uint32_t o[8];
+            for (int k = 0; k < STEPS; ++k) x[k] = ld_shared_v4(from + k * ROWS * D);
+            if (i == PARTS - 1) {
+              __syncwarp();
+              if (lane == 0) mbar_arrive(bar(C::B_REMPTY + rs));  // read: the next tile may come
+            }
 #pragma unroll
-            for (int q = 0; q < 4; ++q) e4m3x4_to_f16x4(w4[q], o[2 * q], o[2 * q + 1]);
-            st_shared_v4(dst + to0 + k * ROWS * C::SWB, make_uint4(o[0], o[1], o[2], o[3]));
-            st_shared_v4(dst + to1 + k * ROWS * C::SWB, make_uint4(o[4], o[5], o[6], o[7]));
+            for (int k = 0; k < STEPS; ++k) {
+              const uint32_t w4[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+              uint32_t o[8];
+#pragma unroll
+              for (int q = 0; q < 4; ++q) e4m3x4_to_f16x4(w4[q], o[2 * q], o[2 * q + 1]);
+              st_shared_v4(part + to0 + k * ROWS * C::SWB, make_uint4(o[0], o[1], o[2], o[3]));
+              st_shared_v4(part + to1 + k * ROWS * C::SWB, make_uint4(o[4], o[5], o[6], o[7]));
+            }
           }
           fence_proxy_async_smem();
           __syncwarp();

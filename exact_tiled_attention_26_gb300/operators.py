@@ -10,7 +10,11 @@ from __future__ import annotations
 
 import torch
 
-from . import tensor_calls as _native
+try:
+    from . import tensor_calls as _native
+except ImportError as e:
+    raise ImportError("tensor_calls.so is missing or does not load: build it with `python "
+                      "exact_tiled_attention_26_gb300/build.py` (or __graft_entry__.build())") from e
 
 _BF16, _I64, _U8, _E4M3 = torch.bfloat16, torch.int64, torch.uint8, torch.float8_e4m3fn
 
