@@ -160,3 +160,50 @@ def test_calls_keep_no_tensor(fa_lib):
     torch.cuda.synchronize()
     after = torch.cuda.memory_allocated(), [sys.getrefcount(t) for t in held], sys.getrefcount(None)
     assert after[:2] == before[:2] and abs(after[2] - before[2]) < 100
+
+
+def test_workspaces_of_the_caller(fa_lib):
+    """A workspace that is large enough is used as it is, a smaller one is not; a misaligned one is refused."""
+    fa = fa_lib
+    g = torch.Generator().manual_seed(5)
+    q = torch.randn(2, 8, 3, 64, generator=g).to(torch.bfloat16).to(DEV)
+    k = torch.randn(2, 2, 3, 64, generator=g).to(torch.bfloat16).to(DEV)
+    cache = fa.new_cache(64, 2, 16, 64)
+    x = torch.randn(2, 2, 500, 64, generator=g).to(torch.bfloat16).to(DEV)
+    table = torch.arange(64, dtype=torch.int32, device=DEV).view(2, 32)
+    lens = torch.tensor([500, 333], dtype=torch.int32, device=DEV)
+    fa.cache_write(cache, x, x, table, lens, lens)
+    want = fa.attention_tree(q, cache, table, lens)
+    n = fa.fa_fwd_tree_workspace_size(2, 8, 2, 3, 64)
+    ws = torch.full((n + 16,), 0xFF, dtype=torch.uint8, device=DEV)
+    for given in (ws[:n], ws[:n], ws[:n - 1], torch.empty(0, dtype=torch.uint8, device=DEV), ws.cpu()):
+        got = fa.attention_tree(q, cache, table, lens, workspace=given)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert not (ws[:n] == 0xFF).all() and (ws[n:] == 0xFF).all()
+    with pytest.raises(fa.FAError):
+        fa.attention_tree(q, cache, table, lens, workspace=ws[1:])
+    w = torch.ones(64, device=DEV)
+    want = fa.qk_norm_rope_backward(q, k, q, k, w, w)
+    n = fa.fa_qk_norm_rope_bwd_workspace_size(2, 8, 2, 3, 64)
+    ws = torch.full((n + 16,), 0xFF, dtype=torch.uint8, device=DEV)
+    for given in (ws[:n], ws[:n - 1]):
+        assert all(torch.equal(a, b) for a, b in zip(fa.qk_norm_rope_backward(q, k, q, k, w, w, workspace=given), want))
+    with pytest.raises(fa.FAError):
+        fa.qk_norm_rope_backward(q, k, q, k, w, w, workspace=ws[1:])
+
+
+def test_views_of_one_projection_and_broadcast_gradients(fa_lib):
+    """q and k as views of one fused projection, gradients that are one row for all: the same as of copies."""
+    fa = fa_lib
+    g = torch.Generator().manual_seed(6)
+    B, N, H, Hk, d = 2, 7, 4, 2, 64
+    qkv = torch.randn(B, N, H + 2 * Hk, d, generator=g).to(torch.bfloat16).to(DEV)
+    q, k = qkv[:, :, :H].transpose(1, 2), qkv[:, :, H:H + Hk].transpose(1, 2)
+    w = (1 + 0.1 * torch.randn(2, d, generator=g)).to(DEV)
+    row = torch.randn(d, generator=g).to(torch.bfloat16).to(DEV)
+    dq, dk = row.expand(B, H, N, d), row.expand(B, Hk, N, d)
+    for a, b in zip(fa.qk_norm_rope(q, k, w[0], w[1]), fa.qk_norm_rope(q.contiguous(), k.contiguous(), w[0], w[1])):
+        assert a.is_contiguous() and torch.equal(a, b)
+    got = fa.qk_norm_rope_backward(q, k, dq, dk, w[0], w[1])
+    want = fa.qk_norm_rope_backward(q.contiguous(), k.contiguous(), dq.contiguous(), dk.contiguous(), w[0], w[1])
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
