@@ -66,5 +66,8 @@ def _rows(t):
 
 
 def qk_norm_rope(q, k, q_weight=None, k_weight=None, cos=None, sin=None, positions=None, eps=1e-6, interleaved=False):
-    """Differentiable qk_norm_rope: q and k of any layout (rows that the kernels cannot take as they lie are copied)."""
+    """Differentiable qk_norm_rope: q and k of any layout (rows that the kernels cannot take as they lie are copied).
+
+    Before a backward is captured into a CUDA graph, let go of every eager graph of the same leaves: PyTorch adds a
+    leaf's gradient on the stream that graph was made on, which a capture on another stream may not touch."""
     return QKNormRopeFunction.apply(_rows(q), _rows(k), q_weight, k_weight, cos, sin, positions, eps, interleaved)
