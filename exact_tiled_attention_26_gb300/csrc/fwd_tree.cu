@@ -665,7 +665,12 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
         const bool warp_live = mt * 128 + (wq * 32) % GR < p.R;
         const unsigned long long* trow =
             p.tree == nullptr ? nullptr : p.tree + w.b * p.tree_stride + static_cast<size_t>(t) * p.words;
-        if (!lead) {  // the scale of its row, from the first warpgroup
+        // The scale of its row, from the first warpgroup.  Only a warp with rows may wait here: the first warpgroup
+        // meets its partner in every tile (B_TOP), so Q's next phase cannot end before this wait has seen its own.  A
+        // warp without rows holds nobody up; it could find that phase passed already and would wait for one that never
+        // comes.  (It has no use for the scale, and S of each unit it goes through was made after that unit's Q, so
+        // that when it has rows again it is no phase behind either.)
+        if (!lead && warp_live) {
           if (!(ok = mbar_rest_warp(bar(C::B_QREADY), seg & 1, guard, SITE_TREE_SOFTMAX))) break;
           q_scale = q_scales[row];
         }

@@ -442,3 +442,33 @@ def test_no_pages_and_no_columns(fa_lib):
         assert not o.any() and torch.isneginf(lse).all()
         k, v = fa.cache_read(cache, table, n, 7)
         assert k.shape == (2, 2, 7, 64) and not k.any() and not v.any()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("G, T", [(8, 5), (8, 9), (8, 17), (4, 63)])  # 40, 72, 136 and 252 rows on a key head
+def test_many_units_on_a_cta(fa_lib, G, T, d, fp8):
+    """Each CTA goes through five units of one to three tiles or more, row tiles with and without rows for all of its
+    warps in turn: every barrier of a unit comes back to each of its phases.  Each call gives the same bits."""
+    fa = fa_lib
+    tiles = (G * T + 127) // 128
+    Hk, page, cols = 2 // tiles, 128, 3
+    B = 420
+    assert B * Hk * tiles >= 5 * 152
+    q, cache, table, g = make(fa, B, Hk * G, Hk, T, d, page, cols, fp8, 71 + d + T)
+    lens = torch.randint(0, 301, (B,), generator=g, dtype=torch.int32)
+    lens[::2] = lens[::2] % 129
+    n_new = torch.randint(0, T + 1, (B,), generator=g, dtype=torch.int32)
+    n_new[::3] = T
+    put(fa, cache, table, lens, g)
+    words, bits = random_tree(B, T, g)
+    args = (q.to(DEV), cache, table.to(DEV), lens.to(DEV), words.to(DEV), n_new.to(DEV))
+    o, lse = fa.attention_tree(*args)
+    st, site = fa.fa_poll_device_error(torch.cuda.current_stream().cuda_stream)
+    assert st == 0, hex(site)
+    for _ in range(20):
+        again = fa.attention_tree(*args)
+        assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
+    some = torch.arange(0, B, 37)
+    compare(o[some], lse[some], q[some], cache, table[some], lens[some], n_new[some], [bits[b] for b in some],
+            1 / math.sqrt(d))
