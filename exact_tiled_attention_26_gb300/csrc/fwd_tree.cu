@@ -50,7 +50,9 @@
 // Keys that are not there (behind the end, in no page) are masked; their values are
 // replaced by zeros before the product, as 0 * NaN would reach every row.  An infinite or
 // NaN value of a drafted token is taken out of the product too and goes only to the
-// rows that see the token (`Poison`).
+// rows that see the token (`Poison`).  An infinite value of the prefix stays in the product,
+// as every row sees it; but where rows are repeated, the groups that weigh its key with zero
+// make NaN of it, so the joining kernel looks into rows that hold a NaN (`mend_rows`).
 #include <cuda_fp16.h>
 
 #include <cmath>
@@ -72,8 +74,9 @@ enum : int { SITE_TREE_PRODUCER = 0x501, SITE_TREE_MMA = 0x502, SITE_TREE_SOFTMA
 // Workspace: for every unit the CTAs that hold its first and last tile, then two partial
 // slots per CTA: [rows][D] fp32 of O, then [3][rows] of m, l, l of the rounded weights.
 struct UnitInfo {
-  int first, last;
+  int first, last;  // first: with kNanUnit where one CTA has all of it and a row holds a NaN that no score explains
 };
+constexpr int kNanUnit = 1 << 16;
 
 struct TreeArgs {
   CacheView c;
@@ -82,7 +85,7 @@ struct TreeArgs {
   float* L;
   const unsigned long long* tree;  // [.., T, words], or null
   long long tree_stride;           // words between sequences
-  int B, G, R, M, words;           // R = G * T rows per key head in M tiles
+  int B, R, M, words;              // R = H / Hk * T rows per key head in M tiles
   int rows;                        // rows of a partial slot: 32, 64 or 128
   float c_log2;
   UnitInfo* info;
@@ -1006,6 +1009,14 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
               }
               const float inv = olr == 0.f ? 0.f : 1.f / olr;
               if (whole) {
+                if constexpr (!FP8) {
+                  bool nan = false;
+#pragma unroll
+                  for (int k = 0; k < EPT; ++k) nan |= a[k] != a[k];
+                  // (the unit's own entry has been written before the barriers above)
+                  if (nan && olr == olr)
+                    p.info[static_cast<long long>(at.b) * hms + at.hm].first = static_cast<int>(blockIdx.x) | kNanUnit;
+                }
                 uint4* dst = reinterpret_cast<uint4*>(p.O + (row0 + orow) * D) + part;
 #pragma unroll
                 for (int k = 0; k < EPT / 8; ++k)
@@ -1128,22 +1139,107 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
   }
 }
 
-// Joins the partial rows of the units that several CTAs share: one warp per row.  Lane k
-// looks after piece k's sums; the rows of O then come eight pieces at a time.
+// Signs of 8 bf16 values: bit e for +inf in element e, bit 8 + e for -inf (a NaN counts as both).
+FA_DEV uint32_t infinities(uint4 v) {
+  const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+  uint32_t signs = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const uint32_t half = x[e / 2] >> (16 * (e & 1)) & 0xffffu;
+    const bool nan = (half & 0x7fffu) > 0x7f80u;
+    if (nan || half == 0x7f80u) signs |= 1u << e;
+    if (nan || half == 0xff80u) signs |= 256u << e;
+  }
+  return signs;
+}
+// A block's rows of a unit, of which some hold a NaN though their sums of weights do not: a NaN element that only
+// infinities of one sign went into becomes infinite, where it has been stored.  All threads of the block call it.  The
+// values are read again, 8 keys a thread under way at once; those of the prefix, which all rows see, once for the
+// block's rows.  Measured: 1.04 ms for 32 rows over 32768 keys
+// (the whole call without an infinite value: 28 us).
 template <int D>
+__noinline__ __device__ void mend_rows(const TreeArgs& p, long long head, int q0, int n) {
+  constexpr int E = D / 32, U = D / 8, STEP = 128 / U;
+  __shared__ uint32_t prefix_signs[2][4];  // bit per element
+  const CacheView& c = p.c;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int b = static_cast<int>(head / c.Hk), h = static_cast<int>(head - static_cast<long long>(b) * c.Hk);
+  const int len = seq_len(c, b), nn = seq_new(c, b), prefix = max(c.lens[b], 0) - nn, inside = min(prefix, len);
+  auto row_of = [&](int page, int j) {
+    return c.V + ((static_cast<size_t>(page) * c.Hk + h) * c.page + (j & (c.page - 1))) * (D * 2);
+  };
+  if (tid < 8) prefix_signs[tid >> 2][tid & 3] = 0u;
+  __syncthreads();
+  uint32_t signs = 0;
+#pragma unroll 1
+  for (long long j0 = tid / U; j0 < inside; j0 += 8 * STEP) {
+    int page[8];
+    uint4 v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) page[i] = j0 + i * STEP < inside ? page_of(c, b, static_cast<int>(j0) + i * STEP) : -1;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      v[i] = page[i] < 0 ? make_uint4(0, 0, 0, 0)
+                         : *reinterpret_cast<const uint4*>(row_of(page[i], static_cast<int>(j0) + i * STEP) + tid % U * 16);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) signs |= infinities(v[i]);
+  }
+  const int unit = tid % U;
+  if (signs & 0xffu) atomicOr(&prefix_signs[0][unit >> 2], (signs & 0xffu) << (8 * (unit & 3)));
+  if (signs >> 8) atomicOr(&prefix_signs[1][unit >> 2], (signs >> 8) << (8 * (unit & 3)));
+  __syncthreads();
+#pragma unroll 1
+  for (int r = blockIdx.y * 4 + (tid >> 5); r < n; r += gridDim.y * 4) {
+    const size_t row = head * p.R + q0 + r;
+    __nv_bfloat16* at = p.O + row * D + lane * E;
+    float o[E];
+    bool nan = false;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = __bfloat162float(at[e]), nan |= o[e] != o[e];
+    // (a NaN score makes all of the row NaN for good)
+    const float L = __shfl_sync(0xffffffffu, lane == 0 ? p.L[row] : 0.f, 0);
+    if (L != L || !__any_sync(0xffffffffu, nan)) continue;
+    const int t = (q0 + r) % c.T, col = lane * E;
+    const unsigned long long* trow =
+        p.tree == nullptr ? nullptr : p.tree + b * p.tree_stride + static_cast<size_t>(t) * p.words;
+    uint32_t plus = prefix_signs[0][col >> 5] >> (col & 31), minus = prefix_signs[1][col >> 5] >> (col & 31);
+#pragma unroll 1
+    for (int j = max(prefix, 0); j < len; ++j) {  // the drafted tokens that the row sees
+      const int page = page_of(c, b, j);
+      if (page < 0 || !(draft_bits(trow, p.words, t, j - prefix) & 1u)) continue;
+      const uint4 v = *reinterpret_cast<const uint4*>(row_of(page, j) + col / 8 * 16);
+      const uint32_t s = infinities(v);
+      plus |= (s & 0xffu) >> (col & 7), minus |= s >> 8 >> (col & 7);
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const bool up = plus >> e & 1u, down = minus >> e & 1u;
+      if (o[e] != o[e] && up != down) at[e] = __float2bfloat16_rn(up ? INFINITY : -INFINITY);
+    }
+  }
+}
+
+// Joins the partial rows of the units that several CTAs share, one warp per row, and puts right the NaNs that
+// infinite values of a bf16 cache left (an e4m3 cache has no infinities).  Lane k
+// looks after piece k's sums; the rows of O then come eight pieces at a time.
+template <int D, bool FP8>
 __global__ void __launch_bounds__(128) tree_join_kernel(const __grid_constant__ TreeArgs p, int grid) {
   constexpr int E = D / 32;  // neighbouring elements of a lane
   pdl_wait();
   const long long unit = blockIdx.x;
-  const UnitInfo u = p.info[unit];
+  UnitInfo u = p.info[unit];
   if (*reinterpret_cast<volatile int*>(p.status) != 0) return;  // the kernel before gave up
-  if (u.last <= u.first || u.first < 0 || u.last >= grid) return;  // finished where it was computed
+  [[maybe_unused]] bool look = false;  // a row may hold a NaN that an infinite value explains
+  if constexpr (!FP8) look = u.first >= 0 && (u.first & kNanUnit) != 0, u.first &= ~kNanUnit;
+  if (u.first < 0 || u.last >= grid || (u.last <= u.first && !look)) return;  // finished where it was computed
   const int lane = threadIdx.x & 31;
   const int mt = p.M == 1 ? 0 : static_cast<int>(unit % p.M);
   const int n = min(128, p.R - mt * 128);
   const size_t slot_size = static_cast<size_t>(p.rows) * (D + 3), sums = static_cast<size_t>(p.rows) * D;
   auto slot = [&](int k) { return p.part + (2 * static_cast<size_t>(k) + (k == u.first ? 1 : 0)) * slot_size; };
+  const long long head = p.M == 1 ? unit : unit / p.M;
   for (int r = blockIdx.y * 4 + (threadIdx.x >> 5); r < n; r += gridDim.y * 4) {
+    if (u.last <= u.first) break;  // (all of it computed by one CTA)
     float mx = -INFINITY, l = 0.f, lr = 0.f, o[E] = {};
     for (int k0 = u.first; k0 <= u.last; k0 += 32) {
       const int k = k0 + lane;
@@ -1194,7 +1290,11 @@ __global__ void __launch_bounds__(128) tree_join_kernel(const __grid_constant__ 
         }
       }
     }
-    const size_t grow = (p.M == 1 ? unit : unit / p.M) * p.R + mt * 128 + r;
+    if constexpr (!FP8) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) look |= o[e] != o[e] && lr == lr;
+    }
+    const size_t grow = head * p.R + mt * 128 + r;
     const float inv = lr == 0.f ? 0.f : 1.f / lr;
     __nv_bfloat16* dst = p.O + grow * D + lane * E;
     if constexpr (E == 4)
@@ -1204,6 +1304,9 @@ __global__ void __launch_bounds__(128) tree_join_kernel(const __grid_constant__ 
     else
       *dst = __float2bfloat16_rn(o[0] * inv);
     if (lane == 0) p.L[grow] = lr == 0.f ? -INFINITY : (mx + lg2(l)) * kFwdLn2;
+  }
+  if constexpr (!FP8) {
+    if (__syncthreads_or(look)) mend_rows<D>(p, head, mt * 128, n);
   }
 }
 
@@ -1240,7 +1343,7 @@ fa_status launch_tree(const TreeArgs& p, int grid, cudaStream_t stream) {
     return FA_ERR_CUDA;
   const unsigned units = static_cast<unsigned>(p.B) * c.Hk * p.M;
   const int n = p.R < 128 ? p.R : 128;
-  const cudaError_t e = launch_pdl(tree_join_kernel<D>, dim3(units, (n + 3) / 4), dim3(128), 0, stream, p, grid);
+  const cudaError_t e = launch_pdl(tree_join_kernel<D, FP8>, dim3(units, (n + 3) / 4), dim3(128), 0, stream, p, grid);
   return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
@@ -1293,7 +1396,7 @@ fa_status fa_fwd_tree(const void* Q, const fa_cache* cache, void* O, float* L, i
   p.L = L;
   p.tree = tree;
   p.tree_stride = B > 1 ? tree_stride : 0;
-  p.B = B, p.G = H / cache->Hk, p.R = static_cast<int>(R), p.M = row_tiles(p.R), p.words = (T + 63) / 64;
+  p.B = B, p.R = static_cast<int>(R), p.M = row_tiles(p.R), p.words = (T + 63) / 64;
   p.rows = slot_rows(p.R);
   p.c_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   const long long units = static_cast<long long>(B) * cache->Hk * p.M;

@@ -337,7 +337,8 @@ fa_status fa_cache_read(const fa_cache* cache, void* K, void* V, int B, int N, c
  *   tree : 64-bit words [B, T, ceil(T/64)], sequences tree_stride words apart (0: one
  *          tree for all); NULL: token t sees tokens 0 .. t.
  * A row that sees no key, and rows t >= n_new[b], get O = 0 and L = -infinity.
- * Values of keys a row does not see never reach it, be they infinite or NaN.
+ * Values of keys a row does not see never reach it, be they infinite or NaN.  An
+ * infinite value that a row sees makes that element infinite (both signs: NaN).
  *   workspace : fa_fwd_tree_workspace_size() bytes, 16-byte aligned (FA_ERR_WORKSPACE
  *               otherwise); calls that overlap on the GPU must not share it.
  */

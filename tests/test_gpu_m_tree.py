@@ -496,3 +496,48 @@ def test_short_e4m3_sequences_hundreds_of_times(fa_lib, G, T, d):
     assert int(differ) == 0
     some = torch.arange(0, B, 53)
     compare(o[some], lse[some], q[some], cache, table[some], lens[some], None, None, 1 / math.sqrt(d))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("G, T", [(1, 1), (4, 1), (33, 1), (66, 1), (2, 3), (8, 5), (8, 9)])
+def test_infinite_values_that_are_seen(fa_lib, G, T, d, fp8):
+    """Infinite values of the prefix, of a single token itself and of drafted tokens, in units of one CTA and of several:
+    infinite of that sign in the rows that see them, NaN where both signs or a NaN meet, and right everywhere else.  (An
+    e4m3 row that holds one is NaN.)"""
+    fa = fa_lib
+    B, Hk, page, cols = 4, 2, 32, 80
+    q, cache, table, g = make(fa, B, Hk * G, Hk, T, d, page, cols, fp8, 81 + d + T + G)
+    lens = torch.tensor([2500, T, 300, 140], dtype=torch.int32)
+    n_new = torch.tensor([T, T, (T + 1) // 2, T], dtype=torch.int32)
+    n = cols * page
+    k, v = (torch.randn(B, Hk, n, d, generator=g).to(torch.bfloat16) for _ in range(2))
+    inf = math.inf
+    v[0, 0, 5, 3], v[0, 0, 1700, 4], v[0, 0, 130, d - 1] = inf, -inf, inf
+    v[0, 0, 900, 9], v[0, 0, 2000, 9], v[0, 0, 2499 - T, 11] = inf, -inf, math.nan
+    v[0, 1, 77, 1] = -inf
+    v[1, 0, 0, 7] = inf                       # the only key, or the first draft
+    v[2, 1, 300 - int(n_new[2]), 6] = -inf    # a token's own value, every live row sees it
+    v[2, 1, 3, 6], v[2, 1, 4, 8] = inf, inf   # the other sign in the prefix
+    v[3, 0, 139, 2], v[3, 1, 139, 2], v[3, 1, 0, 2] = inf, -inf, -inf  # seen by the last draft alone; and a prefix's
+    full = torch.full((B,), n, dtype=torch.int32, device=DEV)
+    fa.cache_write(cache, k.to(DEV), v.to(DEV), table.to(DEV), full)
+    words, bits = random_tree(B, T, g) if T > 1 and d != 32 else (None, None)
+    args = (q.to(DEV), cache, table.to(DEV), lens.to(DEV), None if words is None else words.to(DEV), n_new.to(DEV))
+    o, lse = fa.attention_tree(*args)
+    kv, vv = cache_values(cache)
+    want, want_l, _, dot = orc.tree_attention(q, kv, vv, table, lens, n_new, bits, 1 / math.sqrt(d))
+    got = o.cpu().double()
+    for kind in (torch.isposinf, torch.isneginf, torch.isnan):
+        assert torch.equal(kind(got), kind(want)), kind.__name__
+    # elsewhere the bound of the file's head, with the magnitudes of the finite values
+    vf = torch.where(torch.isfinite(vv), vv, 0.0)
+    _, _, mag, _ = orc.tree_attention(q, kv, vf, table, lens, n_new, bits, 1 / math.sqrt(d))
+    e = 2 * d * 2.0 ** -24 * dot
+    tol = 2.0 ** -8 * want.abs() + (2.0 ** -7 + 2 * e[..., None] + 2.0 ** -14) * mag + 1e-30
+    fine = torch.isfinite(want)
+    assert ((got - want).abs() <= tol)[fine].all()
+    live = ~torch.isneginf(want_l) & ~torch.isnan(want_l)
+    assert ((lse.cpu().double() - want_l).abs() <= e + 2.0 ** -18 * (1 + want_l.abs()))[live].all()
+    again = fa.attention_tree(*args)
+    assert torch.equal(o.nan_to_num(), again[0].nan_to_num()) and torch.equal(lse.nan_to_num(), again[1].nan_to_num())
