@@ -297,6 +297,19 @@ FA_DEV void st_shared_v4(uint32_t at, uint4 v) {
 // starts at 2^kF16Start for a row's largest and the reference moves before it passes
 // 2^kF16Top.  Whatever is 2^-18 of the largest or more keeps 11 bits.
 constexpr float kF16Start = 4.f, kF16Top = 14.f;
+// A value's exponent counts as this at least (its scale stays what it is): a weight is then at most 2^(kF16Top + 83) =
+// 2^97, and 2^30 of them, the longest sequence, stay below fp32's 2^128.  (Rows of zeros have the least exponent, -100.
+// Values below 448 * 2^-83 lose weight bits where none are larger: their largest weights start at 2^-13.)
+constexpr int kRangeMin = 127 - 83;
+// A sum of weights l taken from reference `from` to `to`.  An e4m3 cache's references follow the values' exponents and
+// may lie more than 126 apart, where the factor 2^(from - to) alone would be 0 although l times it is not.
+template <bool FP8>
+FA_DEV float rescaled(float l, float from, float to) {
+  if (from == -INFINITY) return 0.f;
+  if (!FP8) return l * ex2(from - to);
+  const float half = ex2(0.5f * (from - to));
+  return l * half * half;
+}
 
 // Which 16-byte unit of a row the swizzle puts where: unit ^ swz_row(row).
 template <int SWB>
@@ -770,7 +783,10 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
               if (__any_sync(0xffffffffu, move)) {
                 const float new_ref = tile_top + kStart;
                 const float alpha = move ? ex2(ref - new_ref) : 1.f;
-                if (move) l *= alpha, lr *= alpha, ref = new_ref;
+                if (move) {
+                  l = rescaled<FP8>(l, ref, new_ref), lr = FP8 ? l : rescaled<FP8>(lr, ref, new_ref);
+                  ref = new_ref;
+                }
                 // the product that last wrote O is done
                 const int last = pb == 0 ? C::NPB - 1 : pb - 1;
                 if (!(ok = mbar_rest_warp(bar(C::B_PFREE + last), C::NPB == 1 || pb != 0 ? pfree ^ (C::NPB > 1) : pfree, guard,
@@ -990,9 +1006,8 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
 #pragma unroll
               for (int g = 0; g < NS; ++g) {
                 const float mg = rows[g * GR + orow];
-                const float fg = mg == -INFINITY ? 0.f : ex2(mg - om);
-                ol += fg * rows[128 + g * GR + orow];
-                olr += fg * rows[256 + g * GR + orow];
+                ol += rescaled<FP8>(rows[128 + g * GR + orow], mg, om);
+                olr += rescaled<FP8>(rows[256 + g * GR + orow], mg, om);
               }
               if (olr != olr) om = olr;  // so that the join keeps the row
               float a[EPT];
@@ -1085,7 +1100,7 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
             // (bytes below kExpMin are of rows never written, a fresh cache's zeros: with an exponent below -100
             // their unscaled weights would pass fp32's range)
             auto power = [](int e) { return e == kExpNaN ? 1.f : __int_as_float(max(e, kExpMin) << 23); };
-            auto exponent = [](int e) { return e == kExpNaN ? 0.f : static_cast<float>(max(e, kExpMin) - 127); };
+            auto exponent = [](int e) { return e == kExpNaN ? 0.f : static_cast<float>(max(e, kRangeMin) - 127); };
             scale[0] = make_float2(power(ek & 255), power(ek >> 8));
             scale[64] = make_float2(power(ev & 255), power(ev >> 8));
             scale[128] = make_float2(exponent(ev & 255), exponent(ev >> 8));
@@ -1253,13 +1268,19 @@ __global__ void __launch_bounds__(128) tree_join_kernel(const __grid_constant__ 
       for (int i = 16; i > 0; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
       const float old = mx == -INFINITY ? 0.f : ex2(mx - top);  // what the pieces so far are worth now
       const float f = m == -INFINITY ? 0.f : ex2(m - top);
-      pl = f == 0.f ? 0.f : pl * f, plr = f == 0.f ? 0.f : plr * f;
+      if constexpr (FP8)
+        pl = rescaled<FP8>(pl, m, top), plr = rescaled<FP8>(plr, m, top);
+      else
+        pl = f == 0.f ? 0.f : pl * f, plr = f == 0.f ? 0.f : plr * f;
 #pragma unroll
       for (int i = 16; i > 0; i >>= 1) {
         pl += __shfl_xor_sync(0xffffffffu, pl, i);
         plr += __shfl_xor_sync(0xffffffffu, plr, i);
       }
-      l = l * old + pl, lr = lr * old + plr, mx = top;
+      if constexpr (FP8)
+        l = rescaled<FP8>(l, mx, top) + pl, lr = rescaled<FP8>(lr, mx, top) + plr, mx = top;
+      else
+        l = l * old + pl, lr = lr * old + plr, mx = top;
 #pragma unroll
       for (int e = 0; e < E; ++e) o[e] *= old;
       const int cnt = min(32, u.last - k0 + 1);

@@ -541,3 +541,43 @@ def test_infinite_values_that_are_seen(fa_lib, G, T, d, fp8):
     assert ((lse.cpu().double() - want_l).abs() <= e + 2.0 ** -18 * (1 + want_l.abs()))[live].all()
     again = fa.attention_tree(*args)
     assert torch.equal(o.nan_to_num(), again[0].nan_to_num()) and torch.equal(lse.nan_to_num(), again[1].nan_to_num())
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("G, T", [(2, 1), (8, 5), (8, 9)])
+def test_scales_that_change_along_the_sequence(fa_lib, G, T, d):
+    """e4m3 values of size zero first, then of 2^40, 2^-90 and 1, in stretches of 32 keys, of tiles and of many tiles: what
+    the first ones add to the sum of weights counts however small their values are."""
+    fa = fa_lib
+    B, Hk, page, cols = 3, 2, 64, 45
+    q, cache, table, g = make(fa, B, Hk * G, Hk, T, d, page, cols, True, 101 + d + T)
+    lens = torch.tensor([128, 512 + T, 2800], dtype=torch.int32)  # groups of a tile; a CTA's tiles; several CTAs
+    n = cols * page
+    k = torch.randn(B, Hk, n, d, generator=g) * 0.25
+    v = torch.randn(B, Hk, n, d, generator=g)
+    for b, step in enumerate((32, 128, 700)):
+        size = torch.tensor([0.0, 2.0 ** 40, 2.0 ** -90, 1.0])[torch.arange(n) // step % 4]
+        v[b] *= size[:, None]
+    full = torch.full((B,), n, dtype=torch.int32, device=DEV)
+    fa.cache_write(cache, k.to(torch.bfloat16).to(DEV), v.to(torch.bfloat16).to(DEV), table.to(DEV), full)
+    o, lse = fa.attention_tree(q.to(DEV), cache, table.to(DEV), lens.to(DEV))
+    compare(o, lse, q, cache, table, lens, None, None, 1 / math.sqrt(d))
+
+
+@pytest.mark.parametrize("G", [1, 40, 66])
+def test_sums_of_many_weights_stay_finite(fa_lib, G):
+    """65536 keys with values of zero (the least exponent), of which the first 128 score 0 and all others 6.5: their sum
+    of weights is a long way above the first ones'.  As many sequences as SMs, so that a CTA has one to itself."""
+    fa = fa_lib
+    d, page, n, B = 64, 1024, 65536, 152
+    cache = fa.new_cache(n // page, 1, page, d, E4M3)
+    table = torch.arange(n // page, dtype=torch.int32, device=DEV)[None].expand(B, -1)
+    k = torch.full((1, 1, n, d), 0.8125, dtype=torch.bfloat16, device=DEV)
+    k[:, :, :128] = 0
+    lens = torch.full((B,), n, dtype=torch.int32, device=DEV)
+    fa.cache_write(cache, k, torch.zeros_like(k), table[:1], lens[:1])
+    o, lse = fa.attention_tree(torch.ones(B, G, 1, d, dtype=torch.bfloat16, device=DEV), cache, table, lens)
+    want = math.log(128 + (n - 128) * math.exp(6.5))
+    assert not o.any()
+    # exact scores; the sum and its logarithm as in the file's head
+    assert (lse.double() - want).abs().max() <= 2.0 ** -18 * (1 + want)
