@@ -5,7 +5,7 @@
 Each translation unit compiles in parallel into ``_build/``; the objects are
 linked (static CUDA runtime) into ``exact_tiled_attention_26_gb300/libfa_gb300.so``,
 which knows nothing of PyTorch.  ``tensor_calls.so`` beside it is a Python module on
-PyTorch's C++ tensors that calls the library.
+PyTorch's C++ tensors that calls the library; without PyTorch it is left out.
 """
 from __future__ import annotations
 
@@ -38,8 +38,12 @@ def _nvcc() -> str:
 
 
 def _calls_cmd(nvcc):
-    """The compile command of tensor_calls.cpp (PyTorch is found, not imported) and its link command."""
-    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    """The compile command of tensor_calls.cpp (PyTorch is found, not imported) and its link command; None without
+    PyTorch."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        return None
+    torch = os.path.dirname(spec.origin)
     includes = [os.path.join(ROOT, "include"), os.path.join(torch, "include"),
                 os.path.join(torch, "include", "torch", "csrc", "api", "include"), sysconfig.get_paths()["include"],
                 os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include")]
@@ -71,16 +75,19 @@ def build(verbose: bool = False, ptxas_info: bool = False) -> str:
     for src in SOURCES:
         obj = os.path.join(BUILD, src.replace(".cu", ".o"))
         jobs.append((obj, [nvcc, *ARCH, *FLAGS, *extra, "-c", os.path.join(CSRC, src), "-o", obj]))
-    calls_compile, calls_link = _calls_cmd(nvcc)
+    calls_cmd = _calls_cmd(nvcc)
     with ThreadPoolExecutor(max_workers=len(jobs) + 1) as ex:
-        calls = ex.submit(_run, calls_compile, verbose)
+        calls = ex.submit(_run, calls_cmd[0], verbose) if calls_cmd else None
         logs = list(ex.map(lambda j: _run(j[1], verbose), jobs))
-        calls.result()
     tmp = LIB + ".tmp"
     _run([nvcc, *ARCH, "-shared", "-o", tmp, *[j[0] for j in jobs]], verbose)
     os.replace(tmp, LIB)
-    _run(calls_link, verbose)
-    os.replace(CALLS + ".tmp", CALLS)
+    if calls_cmd:  # after the library, which does not depend on it
+        calls.result()
+        _run(calls_cmd[1], verbose)
+        os.replace(CALLS + ".tmp", CALLS)
+    else:
+        print("PyTorch is not installed: tensor_calls.so is not built", file=sys.stderr)
     if ptxas_info:
         print("\n".join(logs))
     return LIB
