@@ -9,8 +9,6 @@ from __future__ import annotations
 import torch
 
 from . import attention_backward, attention_forward
-from .operators import qk_norm_rope as _qk_norm_rope
-from .operators import qk_norm_rope_backward
 
 
 class FlashAttentionFunction(torch.autograd.Function):
@@ -46,14 +44,16 @@ class QKNormRopeFunction(torch.autograd.Function):
     def forward(ctx, q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved):
         ctx.save_for_backward(q, k, q_weight, k_weight, cos, sin, positions)
         ctx.eps, ctx.interleaved = eps, interleaved
-        return _qk_norm_rope(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved)
+        from . import operators  # here, as flash_attention does not need its native module
+        return operators.qk_norm_rope(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved)
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dq_out, dk_out):
         q, k, q_weight, k_weight, cos, sin, positions = ctx.saved_tensors
-        grads = qk_norm_rope_backward(q, k, _rows(dq_out), _rows(dk_out), q_weight, k_weight, cos, sin, positions,
-                                      ctx.eps, ctx.interleaved)
+        from . import operators
+        grads = operators.qk_norm_rope_backward(q, k, _rows(dq_out), _rows(dk_out), q_weight, k_weight, cos, sin,
+                                                positions, ctx.eps, ctx.interleaved)
         return (*grads, None, None, None, None, None)
 
 
