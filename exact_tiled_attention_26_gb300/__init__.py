@@ -27,8 +27,7 @@ __all__ = [
     "attention_forward", "attention_backward", "attention_fwd_bwd_host", "check",
     "FA_CACHE_BF16", "FA_CACHE_E4M3", "fa_cache", "fa_qk_norm_rope", "fa_qk_norm_rope_bwd",
     "fa_qk_norm_rope_bwd_workspace_size", "fa_cache_write", "fa_cache_read", "fa_fwd_tree",
-    "fa_fwd_tree_workspace_size", "KVCache", "new_cache", "qk_norm_rope", "qk_norm_rope_backward", "cache_write",
-    "cache_read", "attention_tree", "tree_words",
+    "fa_fwd_tree_workspace_size",
 ]
 
 FA_OK, FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED, FA_ERR_CUDA, FA_ERR_TIMEOUT, FA_ERR_WORKSPACE = range(6)
@@ -381,7 +380,8 @@ def attention_fwd_bwd_host(q, k, v, do, causal=False, scale=None, window=0, head
 # ------------------------------------------------------------------ around the attention
 
 # KVCache, new_cache, qk_norm_rope, qk_norm_rope_backward, cache_write, cache_read, attention_tree and tree_words live
-# in operators.py, which imports PyTorch: loaded on first use, so that the binding itself does not need it.
+# in operators.py, which imports PyTorch: loaded on first use, so that the binding itself does not need it, and not in
+# __all__, as a star import would load them.
 _OPERATORS = ("KVCache", "new_cache", "qk_norm_rope", "qk_norm_rope_backward", "cache_write", "cache_read",
               "attention_tree", "tree_words")
 
@@ -392,3 +392,7 @@ def __getattr__(name):
     from . import operators
     globals().update((n, getattr(operators, n)) for n in _OPERATORS)
     return globals()[name]
+
+
+def __dir__():
+    return sorted({*globals(), *_OPERATORS})

@@ -28,3 +28,36 @@ except ImportError as e:
 else:
     raise SystemExit('no ImportError')
 """)
+
+
+def test_star_import_without_pytorch(fa_lib):
+    """The C binding as a whole; what needs PyTorch is found by name."""
+    run(f"""
+import sys
+sys.modules['torch'] = None
+from {PKG} import *
+assert fa_version() and callable(fa_fwd_tree) and attention_forward
+import {PKG} as fa
+assert 'attention_tree' in dir(fa) and 'fa_fwd' in dir(fa)
+try:
+    fa.attention_tree
+except ImportError:
+    pass
+else:
+    raise SystemExit('no ImportError')
+""")
+
+
+def test_names_that_are_loaded_when_used(fa_lib):
+    run(f"""
+import {PKG} as fa
+from {PKG} import KVCache, attention_tree, cache_read, cache_write, new_cache, tree_words
+from {PKG} import qk_norm_rope, qk_norm_rope_backward
+assert fa.attention_tree is attention_tree
+try:
+    fa.no_such_name
+except AttributeError:
+    pass
+else:
+    raise SystemExit('no AttributeError')
+""")
