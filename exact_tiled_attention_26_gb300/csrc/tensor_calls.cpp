@@ -307,8 +307,8 @@ PyObject* attention_tree(PyObject* const* a) { /* q ck cv ke ve table lens tree 
     stride = tree->dim() == 3 ? T * W : 0;
   }
   const double scale = a[9] == Py_None ? 1.0 / std::sqrt((double)d) : number(a[9]);
-  const size_t bytes = fa_fwd_tree_workspace_size(t.B, H, c.c.Hk, T, d);
-  if (bytes == (size_t)-1) throw Failed{FA_ERR_INVALID_ARG, "fa_fwd_tree_workspace_size"};
+  size_t bytes = fa_fwd_tree_workspace_size(t.B, H, c.c.Hk, T, d);
+  if (bytes == (size_t)-1) bytes = 0; /* sizes that the call below refuses, with its own status */
   const Tensor ws = workspace_of(a[10], bytes, q);
   Tensor o = at::empty(q.sizes(), q.options()), l = at::empty({t.B, H, T}, q.options().dtype(at::kFloat));
   launch("fa_fwd_tree", c.device, [&](fa_stream_t s) {

@@ -581,3 +581,18 @@ def test_sums_of_many_weights_stay_finite(fa_lib, G):
     assert not o.any()
     # exact scores; the sum and its logarithm as in the file's head
     assert (lse.double() - want).abs().max() <= 2.0 ** -18 * (1 + want)
+
+
+def test_refused_sizes_carry_the_entry_points_status(fa_lib):
+    """What fa_fwd_tree calls unsupported is unsupported from Python too."""
+    fa = fa_lib
+    t, n = torch.zeros(2, 1, dtype=torch.int32, device=DEV), torch.ones(2, dtype=torch.int32, device=DEV)
+
+    def call(H, d, page=16):
+        q = torch.zeros(2, H, 1, d, dtype=torch.bfloat16, device=DEV)
+        return fa.attention_tree(q, fa.new_cache(1, 2, page, d), t, n)
+    for args in ((4, 48), (40000, 32), (4, 64, 24), (4, 96, 16)):
+        with pytest.raises(fa.FAError) as e:
+            call(*args)
+        assert e.value.status == fa.FA_ERR_UNSUPPORTED, args
+    call(4, 64)
