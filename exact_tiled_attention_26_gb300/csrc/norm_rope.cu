@@ -96,6 +96,29 @@ FA_DEV float row_sum(float v) {
   return v;
 }
 
+// Where r = 1 / sqrt(mean(x^2) + eps) lies outside [2^-60, 2^50], a square or their sum may have passed fp32's range.
+// A warp that meets such a row computes it again after its loop, times a power of two (`root_of`, `far_rows`).  The loop
+// pays one subtraction and one maximum a row, on r's bits: at 1 x 32 x 8192 x 128 forward 49.5 to 49.6 us, gradients
+// 75.9 to 76.5; with a branch per row 56.6 and 83.4, with two comparisons 50.6 and 78.8.
+constexpr unsigned kRootMin = 0x21800000u, kRootSpan = 0x58800000u - kRootMin;
+FA_DEV unsigned root_offset(float r) { return static_cast<unsigned>(__float_as_int(r)) - kRootMin; }
+// Scales a row's elements (8 in a lane) by s = 2^-k, for the larger k of its largest element and of sqrt(eps), and
+// returns 1 / sqrt(mean((x s)^2) + eps s^2).  A row of zeros, or with an infinity, is not scaled.
+template <int D>
+FA_DEV float root_of(float (&f)[8], float eps, float* s) {
+  constexpr int LPR = D / 8;
+  float m = 0.f, sq = 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(f[e]));
+#pragma unroll
+  for (int i = LPR / 2; i > 0; i >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, i));
+  const int kx = (__float_as_int(m) >> 23) - 127, ke = eps > 0.f ? ((__float_as_int(eps) >> 23) - 127) >> 1 : -127;
+  *s = m == 0.f || kx == 128 ? 1.f : __int_as_float((127 - min(max(max(kx, ke), -126), 126)) << 23);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) f[e] *= *s, sq = fmaf(f[e], f[e], sq);
+  return rsqrtf(row_sum<LPR>(sq) * (1.f / D) + eps * *s * *s);
+}
+
 // The angles of one lane's 8 elements: out = c * own + s * other, where `other` is the
 // element each is paired with and s carries the sign of the forward rotation.
 // Elements behind `rope` get c = 1, s = 0.
@@ -137,6 +160,90 @@ FA_DEV void load_angles(Angles& a, const NormArgs& p, int position, int col) {
   }
 }
 
+// The rows out of range among those of one warp again, in range, and with GRAD the sums of all its rows for the weight
+// gradients of its columns.  Not inlined: what it needs is found again, so that the loop keeps its registers.
+struct Columns {
+  float v[8];
+};
+template <int D, bool GRAD>
+__noinline__ __device__ Columns far_rows(const NormArgs& p) {
+  constexpr int LPR = D / 8, GPW = 32 / LPR;  // lane groups per warp
+  const bool is_k = blockIdx.x >= static_cast<unsigned>(p.grid_q);
+  const NormTensor& t = p.t[is_k ? 1 : 0];
+  const unsigned block = is_k ? blockIdx.x - p.grid_q : blockIdx.x;
+  const unsigned nblocks = is_k ? gridDim.x - p.grid_q : p.grid_q;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int part = lane % LPR, col = part * 8;
+  const unsigned group = (block * (kThreads / 32) + warp) * GPW + lane / LPR;
+  const unsigned ngroups = nblocks * (kThreads / 32) * GPW;
+  const unsigned hblocks = (t.H + kHeads - 1) / kHeads;
+  const unsigned trips = (t.items + ngroups - 1) / ngroups;
+  const int hchunks = p.rope / 16;
+  const int other_part = p.interleaved || part >= 2 * hchunks ? part : part < hchunks ? part + hchunks : part - hchunks;
+  const int other_lane = lane - part + other_part;
+  float w[8], dw[8] = {};
+  load_weight(t.w, p.w_bf16, col, w);
+#pragma unroll 1
+  for (unsigned trip = 0; trip < trips; ++trip) {
+    const unsigned item = group + trip * ngroups;
+    const bool live = item < t.items;
+    const unsigned bn = live ? item / hblocks : 0, hb = live ? item - bn * hblocks : 0;
+    const unsigned b = bn / p.N, n = bn - b * p.N;
+    const int position = p.pos != nullptr && live ? p.pos[bn] : static_cast<int>(n);
+    Angles a;
+    load_angles(a, p, live ? position : 0, position < 0 ? D : col);
+#pragma unroll 1
+    for (int h = hb * kHeads; h < static_cast<int>(hb * kHeads) + kHeads; ++h) {
+      const bool there = live && h < t.H;
+      float f[8], u[8], o[8], s, sq = 0.f;
+      unpack8(there ? ld_stream(t.x + b * t.sx.b + n * t.sx.n + h * t.sx.h + col) : make_uint4(0, 0, 0, 0), f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sq = fmaf(f[e], f[e], sq);
+      const bool mine = root_offset(rsqrtf(row_sum<LPR>(sq) * (1.f / D) + p.eps)) > kRootSpan && there;
+      if (!GRAD && !__any_sync(0xffffffffu, mine)) continue;
+      const float r = root_of<D>(f, p.eps, &s);
+      if constexpr (GRAD) {
+        unpack8(there ? ld_stream(t.dz + b * t.sdz.b + n * t.sdz.n + h * t.sdz.h + col) : make_uint4(0, 0, 0, 0), u);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) u[e] = f[e] * w[e];
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float across = __shfl_sync(0xffffffffu, u[e], other_lane);
+        o[e] = p.interleaved ? u[e ^ 1] : across;
+      }
+      float res[8], dot = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if constexpr (!GRAD) {
+          res[e] = r * fmaf(u[e], a.c[e], o[e] * a.s[e]);
+        } else {
+          const float dy = fmaf(u[e], a.c[e], -o[e] * a.s[e]);
+          f[e] *= r;
+          if (there && position >= 0) dw[e] = fmaf(dy, f[e], dw[e]);
+          res[e] = dy * w[e];
+          dot = fmaf(res[e], f[e], dot);
+        }
+      }
+      if constexpr (GRAD) {
+        const float along = row_sum<LPR>(dot) * (1.f / D);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) res[e] = r * (res[e] - f[e] * along) * s;
+      }
+      if (position < 0) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) res[e] = 0.f;
+      }
+      if (mine) *reinterpret_cast<uint4*>(t.out + b * t.so.b + n * t.so.n + h * t.so.h + col) = pack8(res);
+    }
+  }
+  Columns sums;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) sums.v[e] = dw[e];
+  return sums;
+}
+
 // GRAD: gradients.  LPR = D / 8 lanes per row.
 template <int D, bool GRAD>
 __global__ void __launch_bounds__(kThreads, kBlocks<GRAD>) norm_rope_kernel(const __grid_constant__ NormArgs p) {
@@ -161,6 +268,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks<GRAD>) norm_rope_kernel(cons
   load_weight(t.w, p.w_bf16, other_part * 8, wo);
 
   float dw[8] = {};
+  unsigned far = 0;  // above kRootSpan: a row out of range
   // every lane of a warp makes the same number of trips (shuffles below)
   const unsigned trips = (t.items + ngroups - 1) / ngroups;
   for (unsigned trip = 0; trip < trips; ++trip) {
@@ -197,6 +305,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks<GRAD>) norm_rope_kernel(cons
 #pragma unroll
       for (int e = 0; e < 8; ++e) sq = fmaf(f[e], f[e], sq);
       const float r = rsqrtf(row_sum<LPR>(sq) * (1.f / D) + p.eps);
+      far = max(far, root_offset(r));
       const uint4 src = GRAD ? gv[i] : xv[i];
       uint4 ov;
       ov.x = __shfl_sync(0xffffffffu, src.x, other_lane);
@@ -237,6 +346,13 @@ __global__ void __launch_bounds__(kThreads, kBlocks<GRAD>) norm_rope_kernel(cons
         for (int e = 0; e < 8; ++e) res[e] = 0.f;
       }
       if (i < nh) *reinterpret_cast<uint4*>(out + i * t.so.h) = pack8(res);
+    }
+  }
+  if (__any_sync(0xffffffffu, far > kRootSpan)) {
+    const Columns all = far_rows<D, GRAD>(p);
+    if constexpr (GRAD) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) dw[e] = all.v[e];
     }
   }
   if constexpr (GRAD) {

@@ -253,7 +253,8 @@ fa_status fa_fwd_bwd_host(const void* Q, const void* K, const void* V, const voi
  *                A row at a negative position is padding: its output is zero.  A
  *                position >= table_rows gives NaN in the rotated elements.
  * Heads counts may differ and may be 0 (that tensor's pointers may then be NULL).
- * eps must be finite and >= 0.
+ * eps must be finite and >= 0.  Rows may have any size that bf16 holds: squares that
+ * pass fp32's range are scaled.  Outputs must not overlap inputs.
  */
 fa_status fa_qk_norm_rope(const void* Q, const void* K, void* Qout, void* Kout, const long long* q_strides,
                           const long long* k_strides, const void* q_weight, const void* k_weight, int weight_bf16,
@@ -269,7 +270,8 @@ fa_status fa_qk_norm_rope(const void* Q, const void* K, void* Qout, void* Kout, 
  *                  rows they are zero.
  *   workspace    : fa_qk_norm_rope_bwd_workspace_size() bytes, 16-byte aligned, when a
  *                  weight gradient is wanted (FA_ERR_WORKSPACE otherwise).
- * Padding rows get a zero gradient and add nothing to the weight gradients.
+ * Padding rows get a zero gradient and add nothing to the weight gradients.  Outputs
+ * must not overlap inputs.
  */
 size_t fa_qk_norm_rope_bwd_workspace_size(int B, int Hq, int Hk, int N, int d);
 fa_status fa_qk_norm_rope_bwd(const void* Q, const void* K, const void* dQout, const void* dKout, void* dQ, void* dK,

@@ -239,3 +239,48 @@ def test_other_stream_and_graph(fa_lib):
     torch.cuda.synchronize()
     for a, b in zip(out, fresh):
         assert (a - b).abs().max() <= 2.0 ** -6 * b.abs().max()
+
+
+@pytest.mark.parametrize("d, rope, interleaved", [(32, 32, False), (64, 16, True), (128, 128, False)])
+@pytest.mark.parametrize("eps", [0.0, 1e-40, 1e-6, 1e30])
+def test_rows_of_any_size(fa_lib, d, rope, interleaved, eps):
+    """Rows whose squares pass fp32's range, up to bf16's largest and down to its least numbers, next to ordinary ones, and
+    an eps anywhere in it: the tolerances of the file's head."""
+    fa = fa_lib
+    g = torch.Generator().manual_seed(d + rope)
+    B, H, Hk, N = 2, 5, 2, 9
+    sizes = [1.0, 1e20, 1e-20, 5e37, 1e-38, 3e-40, 1e10, 1e-30, 0.0]
+
+    def rows(heads):
+        t = torch.randn(B, heads, N, d, generator=g).clamp(-4, 4)
+        return (t * torch.tensor(sizes)[:, None]).to(torch.bfloat16)
+
+    def grads(heads):  # so that dx, about dz / size, is a number of bf16
+        t = torch.randn(B, heads, N, d, generator=g)
+        at = torch.tensor([max(s, 1e-38) for s in sizes], dtype=torch.float64).clamp(1e-3, 1e30)
+        return (t * at[:, None]).to(torch.bfloat16) if eps == 0 else (t * at.clamp(max=1.0)[:, None]).to(torch.bfloat16)
+    q, k, dz, dzk = rows(H), rows(Hk), grads(H), grads(Hk)
+    cos, sin = tables(N, rope)
+    w = 1 + 0.5 * torch.randn(d, generator=g)
+    on = [t.to(DEV) for t in (w, w, cos, sin)]
+    qo, ko = fa.qk_norm_rope(q.to(DEV), k.to(DEV), *on, None, eps, interleaved)
+    got = fa.qk_norm_rope_backward(q.to(DEV), k.to(DEV), dz.to(DEV), dzk.to(DEV), *on, None, eps, interleaved)
+    live = slice(0, N) if eps else slice(0, N - 1)  # a row of zeros has no direction: NaN with eps = 0
+    if not eps:
+        assert qo[:, :, N - 1].isnan().all() and ko[:, :, N - 1].isnan().all()
+    for what, x, z, out, dx, dw in (("q", q, dz, qo, got[0], got[2]), ("k", k, dzk, ko, got[1], got[3])):
+        eps32 = float(torch.tensor(eps, dtype=torch.float32))
+        ref, y = orc.norm_rope(x, w, cos, sin, None, eps32, interleaved)
+        check(out[:, :, live], ref[:, :, live], pair_magnitude(y, rope, interleaved)[:, :, live], 2.0 ** -18, what)
+        rdx, _, mag, _ = orc.norm_rope_grad(x, z, w, cos, sin, None, eps32, interleaved)
+        rdx, mag = rdx[:, :, live], pair_magnitude(mag, rope, interleaved)[:, :, live]
+        top = torch.finfo(torch.bfloat16).max
+        fits = (rdx.abs() + 2.0 ** -17 * mag) < top  # what passes bf16's range is infinite
+        gotx = dx.cpu().double()[:, :, live]
+        err, tol = (gotx - rdx).abs(), 2.0 ** -8 * rdx.abs() + 2.0 ** -17 * mag + 1e-38
+        assert (~fits | (err <= tol)).all(), what
+        _, rdw, _, wmag = orc.norm_rope_grad(x[:, :, live], z[:, :, live], w, cos[live], sin[live], None, eps32, interleaved)
+        if eps:
+            n = B * x.shape[1] * N
+            assert ((dw.cpu().double() - rdw).abs() <= (n + 64) * 2.0 ** -23 * pair_magnitude(wmag, rope, interleaved)
+                    + 2.0 ** -24 * rdw.abs() + 1e-30).all(), what + " weight"
