@@ -284,3 +284,37 @@ def test_rows_of_any_size(fa_lib, d, rope, interleaved, eps):
             n = B * x.shape[1] * N
             assert ((dw.cpu().double() - rdw).abs() <= (n + 64) * 2.0 ** -23 * pair_magnitude(wmag, rope, interleaved)
                     + 2.0 ** -24 * rdw.abs() + 1e-30).all(), what + " weight"
+
+
+@pytest.mark.parametrize("B, H, Hk, N, d, rope, interleaved", [(2, 32, 8, 515, 128, 128, False), (3, 6, 2, 1021, 64, 32, True),
+                                                               (1, 16, 16, 700, 32, 32, False)])
+def test_weight_gradients_within_the_bound_of_their_sums(fa_lib, B, H, Hk, N, d, rope, interleaved):
+    """The bound of the sum that is made, not of one made row by row.  A term passes through at most `depth` additions: 4 rows
+    a step in a lane, the lanes of the warp with the same columns, 8 warps, the blocks in 8 strands, the strands.  Each
+    addition is off by at most 2^-24 of the sum of magnitudes, each term by 2^-18 of its own, a result in fp32 by 2^-24 of
+    itself.  So narrow a bound sees one block's rows missing."""
+    fa = fa_lib
+    g = torch.Generator().manual_seed(B * 7 + d)
+    q, qc = make(B, H, N, d, "bnhd", g, 2.0)
+    k, kc = make(B, Hk, N, d, "bnhd", g, 0.5)
+    dz, dzc = make(B, H, N, d, "bhnd", g)
+    dzk, dzkc = make(B, Hk, N, d, "bhnd", g)
+    cos, sin = tables(N, rope)
+    w = 1 + 0.5 * torch.randn(d, generator=g)
+    on = [t.to(DEV) for t in (w, w, cos, sin)]
+    got = fa.qk_norm_rope_backward(q, k, dz, dzk, *on, None, 1e-6, interleaved)
+    blocks = fa.fa_qk_norm_rope_bwd_workspace_size(B, H, Hk, N, d) // (4 * d)
+    groups = 8 * 32 // (d // 8)  # lane groups of a block, 4 heads of a (batch, row) each step
+    items = [B * N * ((h + 3) // 4) for h in (H, Hk)]
+    for which, (x, z, dw) in enumerate(((qc, dzc, got[2]), (kc, dzkc, got[3]))):
+        mine = max(1, blocks * items[which] // sum(items) - 1)  # at least so many blocks work on this tensor
+        trips = -(-items[which] // (mine * groups))
+        depth = 4 * trips + (32 // (d // 8)).bit_length() + 8 + -(-blocks // 8) + 8
+        _, ref, _, wmag = orc.norm_rope_grad(x, z, w, cos, sin, None, 1e-6, interleaved)
+        bound = (depth * 2.0 ** -24 + 2.0 ** -18) * pair_magnitude(wmag, rope, interleaved) + 2.0 ** -24 * ref.abs()
+        assert ((dw.cpu().double() - ref).abs() <= bound).all(), (which, depth)
+        # without the rows of one block's first step (its groups' 4 heads each)
+        less = z.clone()
+        less.view(B, x.shape[1], N, d)[0, :4, :groups] = 0
+        _, short, _, _ = orc.norm_rope_grad(x, less, w, cos, sin, None, 1e-6, interleaved)
+        assert ((short - ref).abs() > bound).float().mean() > 0.9

@@ -596,3 +596,29 @@ def test_refused_sizes_carry_the_entry_points_status(fa_lib):
             call(*args)
         assert e.value.status == fa.FA_ERR_UNSUPPORTED, args
     call(4, 64)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("H, Hk, T, d, n", [(4, 1, 300, 128, 900), (6, 2, 129, 64, 1500), (2, 2, 1000, 32, 1003)])
+def test_a_chunk_over_the_cache_element_by_element(fa_lib, fp8, H, Hk, T, d, n):
+    """Hundreds of new tokens on several row tiles against fp64, with the bound of the file's head."""
+    fa = fa_lib
+    page = 64
+    cols = (n + page - 1) // page
+    q, cache, table, g = make(fa, 1, H, Hk, T, d, page, cols, fp8, 111 + d)
+    lens = torch.tensor([n], dtype=torch.int32)
+    put(fa, cache, table, lens, g)
+    o, lse = fa.attention_tree(q.to(DEV), cache, table.to(DEV), lens.to(DEV))
+    k, v = (x[0].double() for x in fa.cache_read(cache, table.to(DEV), lens.to(DEV), n))
+    at = torch.arange(n, device=DEV)[None]
+    hidden = at > n - T + torch.arange(T, device=DEV)[:, None]
+    for h in range(H):
+        kk, vv = k[h // (H // Hk)], v[h // (H // Hk)]
+        rows = q[0, h].to(DEV).double()
+        s = (rows @ kk.T / math.sqrt(d)).masked_fill(hidden, -math.inf)
+        e = 2 * d * 2.0 ** -24 * (rows.abs() @ kk.abs().T).amax(-1, keepdim=True) / math.sqrt(d)
+        w = torch.softmax(s, -1)
+        ref, mag = w @ vv, w @ vv.abs()
+        assert ((o[0, h].double() - ref).abs() <= 2.0 ** -8 * ref.abs() + (2.0 ** -7 + 2 * e + 2.0 ** -14) * mag).all(), h
+        L = torch.logsumexp(s, -1)
+        assert ((lse[0, h].double() - L).abs() <= e[:, 0] + 2.0 ** -18 * (1 + L.abs())).all(), h
