@@ -74,7 +74,6 @@ CUtensorMapSwizzle swizzle_for(int inner_bytes) {
   }
 }
 
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 // Shape checks shared by every entry point; *empty is set when there is no work.
 fa_status check_shape(int B, int H, int N, int d, bool* empty) {

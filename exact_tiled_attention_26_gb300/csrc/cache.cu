@@ -29,9 +29,6 @@ constexpr int kRows = 4;      // rows per lane group and step, read and written
 // Rows at a time when reading back: 1, 2, 4, 8: 107, 68.5, 68.2, 68.5 us.
 constexpr int kMaxBlocks = 152 * 64;
 
-struct RowStrides {
-  long long b, h, n;
-};
 struct WriteArgs {
   CacheView c;
   const __nv_bfloat16* x[2];  // new keys, new values
@@ -187,17 +184,6 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_const
       }
     }
   }
-}
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-bool read_strides(const long long* s, int B, int H, int N, int d, RowStrides* out) {
-  if (s == nullptr) {
-    *out = RowStrides{static_cast<long long>(H) * N * d, static_cast<long long>(N) * d, d};
-    return true;
-  }
-  *out = RowStrides{B > 1 ? s[0] : 0, H > 1 ? s[1] : 0, N > 1 ? s[2] : 0};
-  return out->b >= 0 && out->h >= 0 && out->n >= 0 && out->b % 8 == 0 && out->h % 8 == 0 && out->n % 8 == 0;
 }
 
 int blocks_for(long long items, int lanes, int most) {  // lanes: of a row

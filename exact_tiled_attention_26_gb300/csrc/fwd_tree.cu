@@ -1331,8 +1331,6 @@ __global__ void __launch_bounds__(128) tree_join_kernel(const __grid_constant__ 
   }
 }
 
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
 // A cache without a page: no row sees a key.
 __global__ void __launch_bounds__(256) tree_empty_kernel(uint4* O, float* L, long long n16, long long rows) {
   const long long at = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x, step = static_cast<long long>(gridDim.x) * 256;

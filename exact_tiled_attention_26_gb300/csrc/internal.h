@@ -5,6 +5,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
+#include <stdint.h>
 
 #include <utility>
 
@@ -79,6 +80,23 @@ cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t sme
 // Shape and mask checks of the general-mask entry points (fa_fwd_ex's rules);
 // *empty is set when there are no query rows or no heads.
 fa_status check_mask_shape(int B, int H, int Nq, int Nk, int d, int causal, int window, bool* empty);
+inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+// Element strides of a [B,H,N,d] array with contiguous rows (fa.h's `*_strides`).
+struct RowStrides {
+  long long b, h, n;
+};
+// Element strides between batches, heads and rows (null: contiguous [B,H,N,d]); a
+// stride of a dimension of one element is not used.
+inline bool read_strides(const long long* s, int B, int H, int N, int d, RowStrides* out) {
+  if (s == nullptr) {
+    *out = RowStrides{static_cast<long long>(H) * N * d, static_cast<long long>(N) * d, d};
+    return true;
+  }
+  *out = RowStrides{B > 1 ? s[0] : 0, H > 1 ? s[1] : 0, N > 1 ? s[2] : 0};
+  return out->b >= 0 && out->h >= 0 && out->n >= 0 && out->b % 8 == 0 && out->h % 8 == 0 && out->n % 8 == 0;
+}
+
 // scale finite and > 0.
 bool check_scale(float scale);
 

@@ -35,10 +35,6 @@ constexpr int kHeads = 4;  // heads per lane group and step
 template <bool GRAD>
 constexpr int kBlocks = GRAD ? 3 : 4;
 
-struct RowStrides {
-  long long b, h, n;
-};
-
 struct NormTensor {
   const __nv_bfloat16* x;
   const __nv_bfloat16* dz;  // gradients only
@@ -420,18 +416,6 @@ void grid_for(int B, int Hq, int Hk, int N, int d, int blocks[2]) {
     nk = nk > 0 ? most - nq : 0;
   }
   blocks[0] = static_cast<int>(nq), blocks[1] = static_cast<int>(nk);
-}
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-// Element strides between batches, heads and rows (null: contiguous [B,H,N,d]); a
-// stride of a dimension of one element is not used.
-bool read_strides(const long long* s, int B, int H, int N, int d, RowStrides* out) {
-  if (s == nullptr) {
-    *out = RowStrides{static_cast<long long>(H) * N * d, static_cast<long long>(N) * d, d};
-    return true;
-  }
-  *out = RowStrides{B > 1 ? s[0] : 0, H > 1 ? s[1] : 0, N > 1 ? s[2] : 0};
-  return out->b >= 0 && out->h >= 0 && out->n >= 0 && out->b % 8 == 0 && out->h % 8 == 0 && out->n % 8 == 0;
 }
 
 // Checks shared by both directions; *empty: nothing to do.
