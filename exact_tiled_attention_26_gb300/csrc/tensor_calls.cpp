@@ -158,6 +158,8 @@ struct Norm {
       if (!cos) refuse("positions need the cos and sin tables");
       ints(*pos, "positions", {B, N}, device);
     }
+    /* no rows and no positions: tables without an address */
+    if (cos && !cos->size(0) && (!B || !N)) cos = sin = pos = nullptr, rope = 0;
   }
 };
 

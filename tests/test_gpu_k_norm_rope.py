@@ -318,3 +318,20 @@ def test_weight_gradients_within_the_bound_of_their_sums(fa_lib, B, H, Hk, N, d,
         less.view(B, x.shape[1], N, d)[0, :4, :groups] = 0
         _, short, _, _ = orc.norm_rope_grad(x, less, w, cos, sin, None, 1e-6, interleaved)
         assert ((short - ref).abs() > bound).float().mean() > 0.9
+
+
+def test_no_rows_and_no_positions(fa_lib):
+    """An empty batch with tables of no positions: empty outputs, zero weight gradients."""
+    fa = fa_lib
+    w = torch.ones(64, device=DEV)
+    tab = torch.empty(0, 32, device=DEV)
+    for shape in ((2, 4, 0, 64), (0, 4, 8, 64)):
+        q, k = (torch.empty(shape[0], h, *shape[2:], dtype=torch.bfloat16, device=DEV) for h in (4, 2))
+        pos = torch.empty(shape[0], shape[2], dtype=torch.int32, device=DEV)
+        for p in (None, pos):
+            if shape[2] and p is None:
+                continue  # 8 rows, no position for them
+            qo, ko = fa.qk_norm_rope(q, k, w, w, tab, tab, p)
+            assert qo.shape == q.shape and ko.shape == k.shape
+            dq, dk, dqw, dkw = fa.qk_norm_rope_backward(q, k, q, k, w, w, tab, tab, p)
+            assert dq.shape == q.shape and not dqw.any() and not dkw.any()
