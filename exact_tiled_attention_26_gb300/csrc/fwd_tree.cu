@@ -8,13 +8,14 @@
 // A row that sees no key gets O = 0 and L = -inf.
 //
 // The query rows of one key head (G = H / Hk heads of T tokens, contiguous in Q) are the
-// rows of one matrix product, so a key and its value are read once for all of them.
+// rows of one matrix product, 128 at a time: a key and its value are read, and from e4m3
+// converted, once for every 128 of them.
 //
 // Work.  A unit is (sequence, key head, 128-row tile of its rows); it has one tile of 128
-// keys per 128 rows of cache.  The tiles of all units in a row are cut into equal
-// runs, one per CTA, whatever the lengths are (they are only known on the device): every
-// SM reads the same amount of cache, and a single long sequence spreads over the whole
-// GPU.  A unit that lies within one CTA is finished there; the others leave partial
+// keys per 128 rows of cache, also where a long chunk's tokens see only some of them.  The
+// tiles of all units in a row are cut into equal runs, one per CTA, whatever the lengths are
+// (they are only known on the device): every SM reads the same amount of cache, and a single
+// long sequence spreads over the whole GPU.  A unit that lies within one CTA is finished there; the others leave partial
 // rows (O, m, l) in the workspace, at most two per CTA, which a second kernel joins.
 //
 // Rows.  The tensor-core tile has 128 rows.  With at most 32 (or 64) query rows they are
@@ -29,7 +30,8 @@
 // tensor memory); the warpgroup of warps 4..7 puts Q there, runs the softmax and the
 // epilogue.  With more than 64 query rows warps 8..11 are a second one, and the two
 // share a tile's columns: each takes half of a row's 128 scores, they agree on the row's
-// maximum and add their sums at the end (the wide tree below: 124 us with one warpgroup, 96 with two).
+// maximum and add their sums at the end (measured when the second was added, 63 drafts x 4 sequences as below: 124 us
+// with one, 96 with two).
 //
 // An e4m3 cache arrives in a ring of its own; the last warps (8..15, or 12..15) turn its
 // tiles into f16 tiles (one instruction for two elements, exact) and Q is scaled to f16
@@ -38,14 +40,16 @@
 // largest of score + exponent of the value.
 //
 // Measured (d = 128, 8 key heads, 32 query heads, pages read once, device time):
-//   16 sequences up to 32768, a token each, e4m3: 110 us, 4.8 TB/s (0.70 of a plain copy's rate).  A CTA takes some
+//   16 sequences up to 32768, a token each, e4m3: 113 us, 4.7 TB/s (0.69 of a plain copy's rate).  A CTA takes some
 //     1700 cycles a tile where its bytes take 1400: the chain load - convert - S - softmax - P V has five hand-overs a
-//     tile, and the warp that loads K is busy issuing for most of it.
-//   12 drafts x 8 sequences up to 8192, bf16: 36.6 us, 4.1 TB/s; short runs, of which start, unit borders and the join
+//     tile, and the warp that loads K is busy issuing for most of it.  The same from a bf16 cache, without the
+//     conversion and the scales: 6.6 TB/s (0.97).
+//   12 drafts x 8 sequences up to 8192, bf16: 36.5 us, 4.1 TB/s; short runs, of which start, unit borders and the join
 //     are 10 us.
-//   63 drafts x 4 sequences up to 16384, e4m3: 78 us.  Bound by the softmax: every row weighs every key, 6.7e7
-//     exponentials, scaled and packed; then the join of 252-row units, 10 us.
-//   one token over 1000 keys: 9.1 us, two launches and one pass of latencies.
+//   63 drafts x 4 sequences up to 16384, e4m3: 79 us.  252 rows: every tile is loaded, converted and multiplied for two
+//     row tiles in turn, and within each the softmax warps (every row weighs every key, 6.7e7 exponentials, scaled and
+//     packed) and the products wait for one another; then the join, 10 us.
+//   one token over 1000 keys: 9.8 us, two launches and one pass of latencies.
 //
 // Keys that are not there (behind the end, in no page) are masked; their values are
 // replaced by zeros before the product, as 0 * NaN would reach every row.  An infinite or
@@ -155,9 +159,10 @@ FA_DEV long long quotient(long long a, long long b) {
 // A CTA's run.  The units stand one after the other on a line, each with kUnitCost places
 // (what starting and ending a unit costs, in tiles) before its tiles, and the CTAs take
 // equal runs of places: those with a unit's border in them get that many tiles less.
-// Measured for kUnitCost 0 / 3 / 5 / 8: 12 drafts x 8 sequences up to 8192, bf16 44.7 /
-// 38.0 / 36.6 / 36.1 us; 63 drafts x 4 sequences up to 16384, e4m3 104.7 / 95.1 / 91.1 /
-// 92.1; a single token over 1000 keys 9.1 / 9.3 / 9.4 / 9.3.
+// Measured for kUnitCost 0 / 3 / 4 / 6 / 8 / 12: 12 drafts x 8 sequences up to 8192, bf16 46.2 /
+// 38.5 / 38.2 / 37.1 / 36.2 / 37.3 us; 63 drafts x 4 sequences up to 16384, e4m3 91.9 / 81.2 / 80.7 /
+// 77.0 / 78.9 / 80.6; 24 drafts x 4 at d = 64 18.9 / 17.4 / 17.3 / 17.2 / 17.9 / 19.8; 16 tokens up to
+// 32768, e4m3 119.1 / 113.4 / 112.5 / 113.0 / 114.8 / 117.5.
 struct Walk {
   int b, hm, t0, nt;  // sequence, key head and row tile (h * M + mt), first tile, tiles of the unit
   int cost;           // places before the first tile
@@ -488,7 +493,8 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
             if (lane == 0) mbar_expect_tx(full, 128 * D + (kv == 0 ? 2 * n_there * rb : 0));
             const unsigned long long at = static_cast<unsigned long long>(z) * c.page + y;
             // Each lane issues its own box.  With lane 0 issuing all of them in turn the loads of K and the exponents
-            // bound the kernel: 128 us where this takes 114 (16 sequences up to 32768, e4m3), 89 where 83 (63 drafts).
+            // bound the kernel: 119.4 us where this takes 113.0 (16 sequences up to 32768, e4m3), 81.3 where 77.0 (63
+            // drafts).
             __syncwarp();
             if (issues) {
               tma_load_3d(dst + lane * rb * D, map, full, 0, y, z);
@@ -1061,8 +1067,8 @@ __global__ void __launch_bounds__(TCfg<D, FP8, NS>::NTHREADS, 1)
       // tiles are under way at once, as most of a tile's time is waits (its barriers, the fence).
       const int cw = warp - 4 - 4 * C::NW, kv = (cw >> 1) & 1, half = cw >> 2, tid = threadIdx.x & 63;
       constexpr int PPR = D / 16, NP = 2 * PPR;  // 16-byte pieces of an e4m3 row; of a thread
-      // A loop of a few parts, for short code and few registers:
-      // 1 / 2 / 4 parts, 16 sequences of a token each 114 / 110 / 113 us, 63 drafts (one pair of warps) 83 / 80 / 78.
+      // A loop of a few parts, for short code and few registers: 1 / 2 / 4 parts, 16 sequences of a token each 115.4 /
+      // 113.1 / 114.5 us, 63 drafts (one pair of warps) 83.1 / 79.4 / 77.0.
       constexpr int PARTS = C::NPAIR == 1 ? 4 : 2, STEPS = NP / PARTS;
       // Piece `sub` of rows (i * STEPS + k) * ROWS + row.  Eight lanes read 128 bytes of different banks and write 16-byte
       // units of different banks: at d = 128 (two chunks, 8 pieces a row) lanes 4..7 of eight take the upper half of

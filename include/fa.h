@@ -288,7 +288,8 @@ enum {
     FA_CACHE_E4M3 = 1   /* e4m3, one power-of-two scale 2^(byte - 127) per row: the least with
                            max |x| <= 448 * scale, at least 2^-100; magnitudes above 1.875 *
                            2^127 are held as that; byte 255: a row that held an infinity or
-                           a NaN, which reads back as NaN */
+                           a NaN, which reads back as NaN.  (A byte below 27 stands in rows never
+                           written, whose elements are zero.) */
 };
 
 /*
