@@ -310,10 +310,8 @@ constexpr int kRangeMin = 127 - 83;
 // may lie more than 126 apart, where the factor 2^(from - to) alone would be 0 although l times it is not.
 template <bool FP8>
 FA_DEV float rescaled(float l, float from, float to) {
-  if (from == -INFINITY) return 0.f;
-  if (!FP8) return l * ex2(from - to);
-  const float half = ex2(0.5f * (from - to));
-  return l * half * half;
+  const float f = from == -INFINITY ? 0.f : ex2((FP8 ? 0.5f : 1.f) * (from - to));
+  return FP8 ? l * f * f : l * f;
 }
 
 // Which 16-byte unit of a row the swizzle puts where: unit ^ swz_row(row).
