@@ -342,6 +342,10 @@ fa_status fa_cache_read(const fa_cache* cache, void* K, void* V, int B, int N, c
  * A row that sees no key, and rows t >= n_new[b], get O = 0 and L = -infinity.
  * Values of keys a row does not see never reach it, be they infinite or NaN.  An
  * infinite value that a row sees makes that element infinite (both signs: NaN).
+ * Weights enter the product with the values in bf16 (bf16 cache), or times the value's
+ * scale in f16 (e4m3): there a key whose weight times scale is below 2^-18 of the row's
+ * largest loses bits, and below 2^-28 counts for O as nothing.  (That is less than the
+ * largest one's own rounding to e4m3.)
  *   workspace : fa_fwd_tree_workspace_size() bytes, 16-byte aligned (FA_ERR_WORKSPACE
  *               otherwise); calls that overlap on the GPU must not share it.
  */
