@@ -9,8 +9,9 @@
 // mask's order, long ones in parts (split_places).  d = 32 runs with d = 64's tiles, whose second half the loads fill with zeros.
 //
 // What no pair uses may hold anything: a query row that sees no key is zeroed in its tiles before the products with
-// dO and Q (their weights 0 would make NaN of a NaN), an infinite or NaN key is zeroed before dQ^T = K^T dS^T (where
-// a row sees that key, its L is NaN already), and a masked pair's dS is zero whatever dP is.
+// dO and Q (their weights 0 would make NaN of a NaN), an infinite or NaN key is zeroed before dQ^T = K^T dS^T, and a
+// masked pair's dS is zero whatever dP is.  Pairs that see such a key get NaN for P and dS: L need not be NaN there (a
+// score of -infinity has weight 0, a capped one is the cap), and the formula has 0 times infinity.
 //
 // Three launches: D and the cleared dQ sums; the products; dQ rounded to bf16, and split units' parts added.
 //
@@ -61,7 +62,8 @@ struct Stage {
   int pad;
 };
 constexpr int ROFF_RING = ROFF_MISC + 8;
-constexpr int ROFF_STAGE = (ROFF_RING + kRing * static_cast<int>(sizeof(Unit)) + 15) / 16 * 16, RSMALL = ROFF_STAGE + 2 * static_cast<int>(sizeof(Stage));
+constexpr int ROFF_BAD = ROFF_RING + kRing * static_cast<int>(sizeof(Unit));  // [unit parity][4]: see clean_key
+constexpr int ROFF_STAGE = (ROFF_BAD + 2 * 4 * 4 + 15) / 16 * 16, RSMALL = ROFF_STAGE + 2 * static_cast<int>(sizeof(Stage));
 static_assert(RSMALL <= 3 * 1024 && sizeof(Stage) % 16 == 0, "small region");
 
 enum : int { SITE_RB_PRODUCER = 0x611, SITE_RB_MMA = 0x612, SITE_RB_COMPUTE = 0x613, SITE_RB_LAYOUT = 0x615 };
@@ -225,27 +227,49 @@ FA_DEV bool drain(const Ctx& x, int g, float* tile, int nq, int qw, int lane) {
 
 FA_DEV uint32_t not_finite(uint32_t x) { return ((x & 0x7f807f80u) + 0x00800080u) & 0x80008000u; }
 
-// The element-wise threads' share of looking through a unit's K tile: infinities and NaNs become zeros.
+// A unit's K tile, looked through by the element-wise threads, each the row of its key: infinities and NaNs become zeros,
+// for the keys' part in dQ^T of rows that do not see them.  Returns what makes bf16 pairs NaN if the key is not finite,
+// else 0: the scores of such a key are not its own any more (S^T may have been made before or after), and the pairs that
+// see it are made NaN from this.  Half h clears chunk h only.  At d = 128 a chunk is half the row and the other half of the
+// threads may have cleared its own already: it has set the key's bit in `bad` (which the thread's warp and its partner
+// share) before that.
 template <class LY>
-FA_DEV void clean_keys(const Ctx& x, int kvb, int tid) {
-  uint4* at = reinterpret_cast<uint4*>(x.tiles + kvb * LY::KVB) + tid;
-  uint32_t top = 0;
+FA_DEV uint32_t clean_key(const Ctx& x, int kvb, uint32_t* bad, int h, int kr, int lane) {
+  constexpr bool HALVES = LY::TQ == LY::TK;  // (else the second chunk is a copy of the first)
+  uint8_t* row = x.tiles + kvb * LY::KVB + kr * 128;
+  auto look = [&](int c) {
+    uint32_t top = 0;
 #pragma unroll
-  for (int i = 0; i < LY::TK / 16 / NCOMP; ++i) {
-    const uint4 v = at[i * NCOMP];
-    top |= not_finite(v.x) | not_finite(v.y) | not_finite(v.z) | not_finite(v.w);
-  }
-  if (top != 0) {
+    for (int u = 0; u < 8; ++u) {  // (from another place in each lane: a row is 128 bytes, all banks)
+      const uint4 v = *reinterpret_cast<const uint4*>(row + c * CHUNK + 16 * ((u + lane) & 7));
+      top |= not_finite(v.x) | not_finite(v.y) | not_finite(v.z) | not_finite(v.w);
+    }
+    return top;
+  };
+  const uint32_t mine = look(h);
+  uint32_t any = mine;
+  if (HALVES) any |= look(1 - h);
+  if (mine != 0) {
+    if (HALVES) {
+      atomicOr(bad, 1u << lane);
+      __threadfence_block();
+    }
 #pragma unroll 1
-    for (int i = 0; i < LY::TK / 16 / NCOMP; ++i) {
-      const uint4 v = at[i * NCOMP];
+    for (int u = 0; u < 8; ++u) {
+      uint4* at = reinterpret_cast<uint4*>(row + h * CHUNK + 16 * u);
+      const uint4 v = *at;
       uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
       for (int e = 0; e < 4; ++e) w[e] &= ~((not_finite(w[e]) >> 15) * 0xffffu);
-      at[i * NCOMP] = make_uint4(w[0], w[1], w[2], w[3]);
+      *at = make_uint4(w[0], w[1], w[2], w[3]);
     }
     fence_proxy_async_smem();
   }
+  if (HALVES) {
+    __threadfence_block();
+    any |= *reinterpret_cast<volatile uint32_t*>(bad) >> lane & 1u;
+  }
+  return any != 0 ? 0x7fff7fffu : 0u;
 }
 
 // Masks of the pairs of a key with 32 queries: 16 bits of ones for each query that sees it.  R4: the queries' ranges (see
@@ -280,9 +304,11 @@ FA_DEV int split_places(const MaskView& m, int heads, int G, int ctas) {
 }
 
 // Element-wise warps (warp w of 4..11: lane quarter qw = w % 4, query half h = (w-4)/4; one key row per thread): P^T and
-// dS^T of step g.  k_first: first key of the tile; q_first: position of the query tile's first row.
+// dS^T of step g.  k_first: first key of the tile; q_first: position of the query tile's first row.  poison: the key's, of
+// clean_key; any_poison: some key of the warp has one.
 template <class LY, int MOD>
-FA_DEV bool ew_ranges(const Ctx& x, const ScoreMod& mod, int g, int k_first, int q_first, int qw, int h, int lane) {
+FA_DEV bool ew_ranges(const Ctx& x, const ScoreMod& mod, int g, int k_first, int q_first, int qw, int h, int lane,
+                      uint32_t poison, bool any_poison) {
   constexpr bool CAP = (MOD & kModCap) != 0, BIAS = (MOD & kModBias) != 0;
   // (as ew_step: at d = 128 the weights go to the dV product once dP^T is out of tensor memory; with a cap the registers
   // hold half of dP^T at a time)
@@ -298,7 +324,7 @@ FA_DEV bool ew_ranges(const Ctx& x, const ScoreMod& mod, int g, int k_first, int
   const float4* L4 = reinterpret_cast<const float4*>(st->L) + 16 * h;
   const float4* D4 = reinterpret_cast<const float4*>(st->D) + 16 * h;
   const uint4* R4 = reinterpret_cast<const uint4*>(st->ranges) + 8 * h;  // eight rows each
-  const bool masked = st->masked != 0;
+  const bool masked = st->masked != 0 || any_poison;
   // a row's bytes plus these have bit 7 and bit 15 set where the row sees this key (see Stage)
   const uint32_t here = (static_cast<uint32_t>(kr) | static_cast<uint32_t>(127 - kr) << 8) * 0x10001u;
   if (st->dead) {  // (all products that read Q and dO so far are done)
@@ -384,8 +410,8 @@ FA_DEV bool ew_ranges(const Ctx& x, const ScoreMod& mod, int g, int k_first, int
       seen_pairs(R4 + 4 * c, here, see);
 #pragma unroll
       for (int v = 0; v < 16; ++v) {
-        pk[16 * c + v] &= see[v];
-        if constexpr (CAP) pr[16 * c + v] &= see[v];
+        pk[16 * c + v] = (pk[16 * c + v] | poison) & see[v];
+        if constexpr (CAP) pr[16 * c + v] = (pr[16 * c + v] | poison) & see[v];
       }
     }
     tmem_st16(rs + 64 * h + 16 * c, pk + 16 * c);
@@ -527,6 +553,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     tmem_alloc(smem_u32(tmem_slot), TM_COLS);
     tmem_relinquish();
   }
+  uint32_t* bad_keys = reinterpret_cast<uint32_t*>(smem_raw + ROFF_BAD);
+  if (threadIdx.x < 8) bad_keys[threadIdx.x] = 0u;
   if (a.alone) pdl_wait();  // (else: before D is read and before the first sums of dQ)
   if (threadIdx.x == 64) *abort_flag = (*reinterpret_cast<volatile int*>(a.status) != 0);
   tc_fence_before();
@@ -706,10 +734,17 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         }
         const int b = k % NKV;
         if (!(ok = mbar_wait_warp(bar(kvfull(b)), (k / NKV) & 1, x.guard, SITE_RB_COMPUTE))) break;
-        clean_keys<LY>(x, b, threadIdx.x - 128);  // before this unit's first dQ^T, which waits for these warps
+        // before this unit's first dQ^T, which waits for these warps.  The other unit's bits were last read before the steps
+        // of the unit before this one, and are next set after this one's.
+        if (threadIdx.x == 128)
+          for (int e = 0; e < 4; ++e) bad_keys[4 * ((k + 1) & 1) + e] = 0u;
+        const uint32_t poison = clean_key<LY>(x, b, bad_keys + 4 * (k & 1) + qw, h, qw * 32 + lane, lane);
+        const bool any_poison = __any_sync(0xffffffffu, poison != 0);
         const int q_lo = u.lo * BM + m.Nk - m.Nq;
         for (int hq = 0, it = 0; hq < a.G; ++g) {
-          if (!(ok = ew_ranges<LY, MOD>(x, a.mod, g, u.kt * BN, q_lo + it * BM, qw, h, lane))) break;
+          if (!(ok = ew_ranges<LY, MOD>(x, a.mod, g, u.kt * BN, q_lo + it * BM, qw, h, lane, poison,
+                                        any_poison)))
+            break;
           if (++it == u.n) it = 0, ++hq;
         }
         if (!ok) break;

@@ -432,9 +432,10 @@ fa_status fa_fwd_ranges(const void* Q, const void* K, const void* V, void* O, fl
  *   workspace : fa_bwd_ranges_workspace_size() bytes, 16-byte aligned (FA_ERR_WORKSPACE
  *        otherwise); calls that overlap on the GPU must not share it.
  * Rows that see no key and keys that no row sees get zero gradients and may hold anything:
- * nothing of them (nor of their dO) reaches the other gradients.  (An infinity or NaN in a row
- * or key that takes part makes gradients NaN, also of keys and rows near it that it does not
- * see.)  dQ's sums over key tiles are fp32 additions in no fixed order; dK and dV are the
+ * nothing of them (nor of their dO) reaches the other gradients.  An infinite or NaN key that
+ * rows see makes its dK and dV and those rows' dQ NaN (and, where L is NaN, the gradients of
+ * what these rows see).  (An infinity or NaN in a row of Q or dO, or in a value, that takes part
+ * makes gradients NaN, also of keys and rows near it that it does not see.)  dQ's sums over key tiles are fp32 additions in no fixed order; dK and dV are the
  * same on every run.  Slopes are constants: they have no gradient.
  */
 size_t fa_bwd_ranges_workspace_size(int B, int H, int Hk, int Nq, int Nk, int d);
