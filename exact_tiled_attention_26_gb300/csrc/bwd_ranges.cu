@@ -78,7 +78,6 @@ struct BwdRangesArgs {
   float* part;  // [split units][kParts][2][128][D]: dK and dV of a unit's parts
   int H, Hk, G, qh, qb, kh, kb, vh, vb, gh, gb;  // (…h, …b: 0 where the tensor's heads, batches have stride 0)
   float scale;
-  int alone;  // no kernel of this call runs before this one
   int* status;
 };
 
@@ -555,7 +554,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   }
   uint32_t* bad_keys = reinterpret_cast<uint32_t*>(smem_raw + ROFF_BAD);
   if (threadIdx.x < 8) bad_keys[threadIdx.x] = 0u;
-  if (a.alone) pdl_wait();  // (else: before D is read and before the first sums of dQ)
+  // (pdl_wait: before D is read and before the first sums of dQ)
   if (threadIdx.x == 64) *abort_flag = (*reinterpret_cast<volatile int*>(a.status) != 0);
   tc_fence_before();
   __syncthreads();
@@ -903,35 +902,31 @@ fa_status launch(const RangesLaunch& a) {
   int dev = 0, nsm = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return FA_ERR_CUDA;
-  if (rows > 0) {
-    const long long blocks = (rows + 256 / (DR / 8) - 1) / (256 / (DR / 8)), most = 8LL * nsm;
-    if (launch_pdl(bwd_ranges_prepare<DR>, dim3(static_cast<unsigned>(blocks < most ? blocks : most)), dim3(256), 0,
-                   a.stream, static_cast<const __nv_bfloat16*>(a.O), static_cast<const __nv_bfloat16*>(a.dO), a.sdo, a.Lin,
-                   Dbuf, acc, a.H, a.Nq, rows) != cudaSuccess)
-      return FA_ERR_CUDA;
-  }
+  const long long row_blocks = (rows + 256 / (DR / 8) - 1) / (256 / (DR / 8)), most_blocks = 8LL * nsm;
+  if (launch_pdl(bwd_ranges_prepare<DR>, dim3(static_cast<unsigned>(row_blocks < most_blocks ? row_blocks : most_blocks)),
+                 dim3(256), 0, a.stream, static_cast<const __nv_bfloat16*>(a.O), static_cast<const __nv_bfloat16*>(a.dO),
+                 a.sdo, a.Lin, Dbuf, acc, a.H, a.Nq, rows) != cudaSuccess)
+    return FA_ERR_CUDA;
   const long long units = static_cast<long long>(a.B) * a.mask.Tk * a.Hk;
   if (units > INT_MAX / 2) return FA_ERR_UNSUPPORTED;
   const int most = most_ctas(a.B, a.Hk, a.Nk), grid = most < nsm ? most : nsm;
   const BwdRangesArgs args{a.mask, a.mod, a.Lin, Dbuf, acc, static_cast<__nv_bfloat16*>(a.dK),
-                           static_cast<__nv_bfloat16*>(a.dV), reinterpret_cast<float*>(a.workspace + w.part), a.H, a.Hk, units > 0 ? a.H / a.Hk : 1,
+                           static_cast<__nv_bfloat16*>(a.dV), reinterpret_cast<float*>(a.workspace + w.part), a.H, a.Hk, a.H / a.Hk,
                            a.sq.h != 0, a.sq.b != 0, a.sk.h != 0, a.sk.b != 0, a.sv.h != 0, a.sv.b != 0, a.sdo.h != 0,
-                           a.sdo.b != 0, a.scale, rows == 0, a.status};
+                           a.sdo.b != 0, a.scale, a.status};
   if (units > 0) {
     CUtensorMap mQ, mK, mV, mdO;
     if (!encode_bf16_rows(&mK, a.K, DR, a.Nk, a.Hk, a.B, a.sk, 64, BN) ||
         !encode_bf16_rows(&mV, a.V, DR, a.Nk, a.Hk, a.B, a.sv, 64, BN) ||
-        (rows > 0 && (!encode_bf16_rows(&mQ, a.Q, DR, a.Nq, a.H, a.B, a.sq, 64, BM) ||
-                      !encode_bf16_rows(&mdO, a.dO, DR, a.Nq, a.H, a.B, a.sdo, 64, BM))))
+        !encode_bf16_rows(&mQ, a.Q, DR, a.Nq, a.H, a.B, a.sq, 64, BM) ||
+        !encode_bf16_rows(&mdO, a.dO, DR, a.Nq, a.H, a.B, a.sdo, 64, BM))
       return FA_ERR_CUDA;
-    if (rows == 0) mQ = mdO = mK;  // (no step reads them)
     auto kern = bwd_ranges_kernel<D, DR, MOD>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, LY::SMEM) != cudaSuccess)
       return FA_ERR_CUDA;
     if (launch_pdl(kern, dim3(grid), dim3(NTHREADS), LY::SMEM, a.stream, mQ, mK, mV, mdO, args) != cudaSuccess)
       return FA_ERR_CUDA;
   }
-  if (rows == 0) return FA_OK;
   const long long n8 = rows * DR / 8, blocks = (n8 + 255) / 256;
   const int ctas = units > 0 ? grid : 0, converts = static_cast<int>(blocks < 16LL * nsm ? blocks : 16LL * nsm);
   return launch_pdl(bwd_ranges_finish<D, DR>, dim3(ctas * kJoin + converts), dim3(256), 0, a.stream, args,
@@ -951,6 +946,11 @@ fa_status launch_mod(const RangesLaunch& a) {
 size_t bwd_ranges_workspace(int B, int H, int Hk, int Nq, int Nk, int d) { return work_of(B, H, Hk, Nq, Nk, d).bytes; }
 
 fa_status launch_bwd_ranges(const RangesLaunch& a) {
+  if (a.Nq == 0 || a.H == 0) {  // no row, whatever the mask lists (B, Hk and Nk are not 0: fa_bwd_ranges)
+    const size_t bytes = static_cast<size_t>(a.B) * a.Hk * a.Nk * a.d * 2;
+    const fa_status st = launch_zero(a.dK, bytes, a.stream);
+    return st != FA_OK ? st : launch_zero(a.dV, bytes, a.stream);
+  }
   return a.d == 32 ? launch_mod<64, 32>(a) : a.d == 64 ? launch_mod<64, 64>(a) : launch_mod<128, 128>(a);
 }
 

@@ -1,4 +1,5 @@
-"""Attention over ranges of keys at the limits of what it takes: keys that are not finite in the gradients.
+"""Attention over ranges of keys at the limits of what it takes: keys that are not finite in the gradients, no
+query heads.
 
 Bounds as in test_gpu_o_ranges.py and oracle/ranges.py.
 """
@@ -61,4 +62,26 @@ def test_gradients_of_a_key_that_is_not_finite(fa_lib, d, cap, value):
         _, dk2, dv2 = fa.attention_ranges_backward(q, bad, v, o, lse, do, m, softcap=cap)
         assert torch.equal(dk.isnan(), dk2.isnan()) and torch.equal(dk.nan_to_num(), dk2.nan_to_num())
         assert torch.equal(dv.isnan(), dv2.isnan()) and torch.equal(dv.nan_to_num(), dv2.nan_to_num())
+    clean_status(fa)
+
+
+# ------------------------------------------------------------------ no rows
+
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("B,H,Hk,Nq,Nk", [(2, 0, 2, 5, 5), (2, 0, 2, 300, 1000), (1, 4, 2, 0, 129), (3, 0, 1, 0, 1)])
+def test_no_query_rows_give_keys_no_gradients(fa_lib, B, H, Hk, Nq, Nk, d):
+    fa = fa_lib
+    q = torch.ones(B, H, Nq, d, dtype=torch.bfloat16, device=DEV)
+    k, v = (torch.ones(B, Hk, Nk, d, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    lse = torch.zeros(B, H, Nq, device=DEV)
+    m = fa.mask_ranges(B, Nq, Nk)
+    ws = torch.empty(fa.fa_bwd_ranges_workspace_size(B, H, Hk, Nq, Nk, d), dtype=torch.uint8, device=DEV)
+    dk, dv = (torch.full_like(k, 7.0) for _ in range(2))
+    stream = torch.cuda.current_stream().cuda_stream
+    status = fa.fa_bwd_ranges(0, k.data_ptr(), v.data_ptr(), 0, 0, 0, 0, dk.data_ptr(), dv.data_ptr(), None, None, None,
+                              None, m.buffer.data_ptr(), m.buffer.nbytes, B, H, Hk, Nq, Nk, d, 0.0, None, 1.0,
+                              ws.data_ptr(), ws.nbytes, stream)
+    assert status == 0 and not dk.any() and not dv.any()
+    dq, dk, dv = fa.attention_ranges_backward(q, k, v, q, lse, q, m)
+    assert dq.shape == q.shape and not dk.any() and not dv.any()
     clean_status(fa)
