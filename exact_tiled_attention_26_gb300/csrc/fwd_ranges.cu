@@ -142,19 +142,21 @@ FA_DEV void zero_masked(uint32_t tS, const uint32_t (&see)[2]) {
   tmem_st_wait();
 }
 
-// Capped scores in tensor memory, each by itself.
-FA_DEV void cap_in_place(uint32_t tS, const CapArgs& cap) {
+// Capped scores in tensor memory, each by itself but in rows that are `fast` (whose bits are not to depend on the other
+// rows of the warp).  From the scores again: a warp that kept its fast ones meanwhile took 6 % longer in all tiles.
+FA_DEV void cap_in_place(uint32_t tS, const CapArgs& cap, bool fast) {
 #pragma unroll 1
   for (int c = 0; c < 4; ++c) {
     uint32_t r[16];
-    float s[16];
+    float s[16], t[16];
     tmem_ld16(tS + 16 * c, r);
     tmem_ld_wait<16>(r);
 #pragma unroll
-    for (int k = 0; k < 16; ++k) s[k] = __uint_as_float(r[k]);
+    for (int k = 0; k < 16; ++k) s[k] = t[k] = __uint_as_float(r[k]);
     cap_scores(s, cap);
+    cap_scores_fast(t, cap);
 #pragma unroll
-    for (int k = 0; k < 16; ++k) r[k] = __float_as_uint(s[k]);
+    for (int k = 0; k < 16; ++k) r[k] = __float_as_uint(fast ? t[k] : s[k]);
     tmem_st16(tS + 16 * c, r);
   }
   tmem_st_wait();
@@ -225,8 +227,9 @@ FA_DEV bool ranges_half(SoftmaxRow& st, uint32_t tS, uint32_t tO, int half, bool
   load_scores(s, tS);
   if constexpr (MOD != kModNone) {
     if constexpr ((MOD & kModCap) != 0) {
-      if (!__all_sync(0xffffffffu, cap_scores_fast(s, mod.cap))) {
-        cap_in_place(tS, mod.cap);
+      const bool fast = cap_scores_fast(s, mod.cap);
+      if (!__all_sync(0xffffffffu, fast)) {
+        cap_in_place(tS, mod.cap, fast);
         load_scores(s, tS);
       }
     }

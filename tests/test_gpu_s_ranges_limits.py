@@ -1,5 +1,5 @@
 """Attention over ranges of keys at the limits of what it takes: keys that are not finite in the gradients, no
-query heads.
+query heads, scores far beyond the cap.
 
 Bounds as in test_gpu_o_ranges.py and oracle/ranges.py.
 """
@@ -84,4 +84,30 @@ def test_no_query_rows_give_keys_no_gradients(fa_lib, B, H, Hk, Nq, Nk, d):
     assert status == 0 and not dk.any() and not dv.any()
     dq, dk, dv = fa.attention_ranges_backward(q, k, v, q, lse, q, m)
     assert dq.shape == q.shape and not dk.any() and not dv.any()
+    clean_status(fa)
+
+
+# ------------------------------------------------------------------ scores far beyond the cap
+
+@pytest.mark.parametrize("d,bias", [(32, False), (64, True), (128, False)])
+def test_large_scores_of_other_rows_do_not_show(fa_lib, d, bias):
+    """Rows 0 .. 39 and 40 .. 299 are documents of their own, and some of the second have scores of hundreds of caps, or
+    see a key that is not finite: the others' bits stay.  (Rows 32 .. 63 share a warp.)"""
+    fa = fa_lib
+    H, Hk, N = 4, 2, 300
+    g = torch.Generator().manual_seed(17)
+    q, k, v = rand(g, 1, H, N, d, mult=2.0), rand(g, 1, Hk, N, d), rand(g, 1, Hk, N, d)
+    slopes = torch.rand(H, generator=g).to(DEV) * 0.01 if bias else None
+    m = fa.mask_ranges(1, N, causal=True, documents=i32([[0, 40, 300]]))
+    want, wl = fa.attention_ranges(q, k, v, m, softcap=0.5, slopes=slopes)
+    big = q.clone()
+    loud = torch.zeros(N, dtype=torch.bool, device=DEV)
+    loud[41::3] = True
+    big[:, :, loud] *= 512.0
+    o, lse = fa.attention_ranges(big, k, v, m, softcap=0.5, slopes=slopes)
+    assert torch.equal(o[:, :, ~loud], want[:, :, ~loud]) and torch.equal(lse[:, :, ~loud], wl[:, :, ~loud])
+    bad = k.clone()
+    bad[:, :, 60] = NAN
+    o, lse = fa.attention_ranges(q, bad, v, m, softcap=0.5, slopes=slopes)
+    assert torch.equal(o[:, :, :60], want[:, :, :60]) and torch.equal(lse[:, :, :60], wl[:, :, :60])
     clean_status(fa)
