@@ -77,7 +77,7 @@ struct BwdRangesArgs {
   __nv_bfloat16 *dK, *dV;
   float* part;  // [split units][kParts][2][128][D]: dK and dV of a unit's parts
   int H, Hk, G, qh, qb, kh, kb, vh, vb, gh, gb;  // (…h, …b: 0 where the tensor's heads, batches have stride 0)
-  float scale;
+  float scale;  // of dQ's and dK's sums (with a cap, dS is over kRateScale)
   int* status;
 };
 
@@ -354,14 +354,10 @@ FA_DEV bool ew_ranges(const Ctx& x, const ScoreMod& mod, int g, int k_first, int
     float sc[32];
 #pragma unroll
     for (int v = 0; v < 32; ++v) sc[v] = __uint_as_float(r[v]);
-    if constexpr (CAP) cap_scores(sc, mod.cap);
-    [[maybe_unused]] float th[CAP && BIAS ? 32 : 1];  // the capped scores before their bias
+    [[maybe_unused]] float rate[CAP ? 32 : 1];  // 1 - tanh^2, over kRateScale
+    if constexpr (CAP) cap_scores_rate(sc, rate, mod.cap);
     if constexpr (BIAS) {
       const float dist = static_cast<float>(d0 + 32 * c);
-      if constexpr (CAP) {
-#pragma unroll
-        for (int v = 0; v < 32; ++v) th[v] = sc[v];
-      }
       if (side != 0) {
         const float at = -ss * dist;
         const uint64_t step = f2pack(-2.f * ss, -2.f * ss);
@@ -395,10 +391,8 @@ FA_DEV bool ew_ranges(const Ctx& x, const ScoreMod& mod, int g, int k_first, int
           float p0 = ex2(t0), p1 = ex2(t1);
           pk[16 * c + (xx >> 1)] = pack_bf16x2(p0, p1);
           if constexpr (CAP) {
-            const uint64_t x = BIAS ? f2pack(th[BIAS ? xx : 0], th[BIAS ? xx + 1 : 0]) : x2;
-            const uint64_t t = fmul2(x, f2pack(mod.cap.inv_cap, mod.cap.inv_cap));  // r = 1 - tanh^2
             float q0, q1;
-            f2unpack(fmul2(f2pack(p0, p1), ffma2(t, fmul2(t, f2pack(-1.f, -1.f)), f2pack(1.f, 1.f))), q0, q1);
+            f2unpack(fmul2(f2pack(p0, p1), f2pack(rate[xx], rate[xx + 1])), q0, q1);
             pr[16 * c + (xx >> 1)] = pack_bf16x2(q0, q1);
           }
         }
@@ -913,7 +907,7 @@ fa_status launch(const RangesLaunch& a) {
   const BwdRangesArgs args{a.mask, a.mod, a.Lin, Dbuf, acc, static_cast<__nv_bfloat16*>(a.dK),
                            static_cast<__nv_bfloat16*>(a.dV), reinterpret_cast<float*>(a.workspace + w.part), a.H, a.Hk, a.H / a.Hk,
                            a.sq.h != 0, a.sq.b != 0, a.sk.h != 0, a.sk.b != 0, a.sv.h != 0, a.sv.b != 0, a.sdo.h != 0,
-                           a.sdo.b != 0, a.scale, a.status};
+                           a.sdo.b != 0, a.scale * (MOD & kModCap ? kRateScale : 1.f), a.status};
   if (units > 0) {
     CUtensorMap mQ, mK, mV, mdO;
     if (!encode_bf16_rows(&mK, a.K, DR, a.Nk, a.Hk, a.B, a.sk, 64, BN) ||

@@ -15,15 +15,13 @@ namespace fa {
 // a polynomial of degree 13 where no score passes the cap 2.69, for every other pair of scores 2.48.
 struct CapArgs {
   float cap_log2;  // cap log2 e; 0: no cap
-  float inv_cap;   // 1 / cap_log2
   float to_y;      // y = x to_y
 };
 // unit: what x is multiplied by to be a score s.
 inline CapArgs cap_args(double cap, double unit) {
   constexpr double log2e = 1.4426950408889634;
-  if (!(cap > 0.0)) return CapArgs{0.f, 0.f, 0.f};
-  return CapArgs{static_cast<float>(cap * log2e), static_cast<float>(1.0 / (cap * log2e)),
-                 static_cast<float>(2.0 * log2e * unit / cap)};
+  if (!(cap > 0.0)) return CapArgs{0.f, 0.f};
+  return CapArgs{static_cast<float>(cap * log2e), static_cast<float>(2.0 * log2e * unit / cap)};
 }
 
 // x becomes the capped score in base 2.
@@ -37,6 +35,27 @@ FA_DEV void cap_scores(float (&x)[N], const CapArgs& c) {
     f2unpack(fmul2(f2pack(x[k], x[k + 1]), to2), y0, y1);
     f2unpack(fadd2(f2pack(ex2(y0), ex2(y1)), one2), a0, a1);
     f2unpack(ffma2(f2pack(rcp(a0), rcp(a1)), m2, cap2), x[k], x[k + 1]);
+  }
+}
+
+// The same for the gradients, with the cap's derivative:
+//   tanh = +-(1 - 2 w), 1 - tanh^2 = 4 (w - w^2), w = 1 / (1 + 2^|y|),
+// which keeps its relative precision however far a score is beyond the cap, as w <= 1/2 (of 1 - tanh^2 itself some 2^-23
+// would be left there).  `rate` is the derivative times 1 / kRateScale: w^2 - w is one operation from -w.
+constexpr float kRateScale = -4.f;
+template <int N>
+FA_DEV void cap_scores_rate(float (&x)[N], float (&rate)[N], const CapArgs& c) {
+  const uint64_t to2 = f2pack(c.to_y, c.to_y), cap2 = f2pack(c.cap_log2, c.cap_log2);
+  const uint64_t m2 = f2pack(2.f * c.cap_log2, 2.f * c.cap_log2), minus2 = f2pack(-1.f, -1.f);
+#pragma unroll
+  for (int k = 0; k < N; k += 2) {
+    float y0, y1, a0, a1, s0, s1;
+    f2unpack(fmul2(f2pack(x[k], x[k + 1]), to2), y0, y1);
+    f2unpack(ffma2(f2pack(ex2(fabsf(y0)), ex2(fabsf(y1))), minus2, minus2), a0, a1);
+    const uint64_t w = f2pack(rcp(a0), rcp(a1));  // -w
+    f2unpack(ffma2(w, m2, cap2), s0, s1);
+    x[k] = copysignf(s0, y0), x[k + 1] = copysignf(s1, y1);
+    f2unpack(ffma2(w, w, w), rate[k], rate[k + 1]);
   }
 }
 

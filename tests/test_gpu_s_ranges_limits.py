@@ -1,5 +1,5 @@
 """Attention over ranges of keys at the limits of what it takes: keys that are not finite in the gradients, no
-query heads, scores far beyond the cap.
+query heads, scores far beyond the cap, masks far from their rows.
 
 Bounds as in test_gpu_o_ranges.py and oracle/ranges.py.
 """
@@ -9,7 +9,7 @@ import pytest
 import torch
 
 from oracle import ranges as orc
-from test_gpu_o_ranges import close, rand
+from test_gpu_o_ranges import check, close, rand
 from test_gpu_q_ranges_edges import INF, NAN, clean_status, i32
 
 pytestmark = pytest.mark.gpu
@@ -111,3 +111,85 @@ def test_large_scores_of_other_rows_do_not_show(fa_lib, d, bias):
     o, lse = fa.attention_ranges(q, bad, v, m, softcap=0.5, slopes=slopes)
     assert torch.equal(o[:, :, :60], want[:, :, :60]) and torch.equal(lse[:, :, :60], wl[:, :, :60])
     clean_status(fa)
+
+
+def capped_reference(q, k, v, do, m, scale, cap, slopes):
+    """O, L, dQ, dK, dV in 64 bits, each with its bound.
+
+    A score before the cap is off by its products' and sums' roundings, d 2^-24 of size = sum |q k| scale; after it by that
+    times the derivative (times 1.25: it is up to a tenth of the cap here, and e^0.2 < 1.25), 2^-19 cap, and 2^-22 of the
+    bias.  With 2^-18 of the exponentials this is eps.  The derivative 4 w (1 - w) is off by rr of it: twice the score's error
+    over the cap, the rounding of 2 log2 e s / cap (4 2^-24 of it), 2^-19 of the exponential and the reciprocal.  A weight
+    (times the derivative), dS, O and the results are rounded to bf16, 2^-8 each; sums of fp32 are off by 2^-14.  What is
+    below 2^-126 on the way may become 0: less than 2^-100 in a result, whose other factors are below 2^10 in sums of 300."""
+    H, Hk, d, N = q.shape[1], k.shape[1], q.shape[-1], q.shape[2]
+    tiny = 2.0 ** -100
+    s, _, size = orc._scores(q, k, m.first, m.last, scale, cap, slopes)
+    raw = (q.double().view(*k.shape[:2], H // Hk, N, d) @ k.double()[:, :, None].transpose(-1, -2)).view_as(s) * scale
+    u = torch.exp(-2 * raw.abs() / cap)
+    rate = 4 * u / (1 + u) ** 2  # (1 - tanh^2 is 0 in 64 bits from 19 caps on)
+    p, lse = orc._softmax(s)
+    bias = 0.0 if slopes is None else float(slopes.abs().max()) * N
+    eps = (d * 2.0 ** -24 * 1.25 * size * rate).amax(-1, keepdim=True) + 2.0 ** -19 * cap + 2.0 ** -22 * bias + 2.0 ** -18
+    rr = 2 * (d + 4) * 2.0 ** -24 * size / cap + 2.0 ** -19
+    qf, kf, vf, g = q.double(), orc._heads(k, H), orc._heads(v, H), do.double()
+    o, mag = p @ vf, p @ vf.abs()
+    off_o = 2.0 ** -8 * o.abs() + (2.0 ** -7 + 2 * eps) * mag + tiny
+    dp, D = g @ vf.transpose(-1, -2), (g * o).sum(-1, keepdim=True)
+    off_d = (g.abs() * (off_o + 2.0 ** -14 * o.abs())).sum(-1, keepdim=True) + 2.0 ** -14 * (g.abs() @ vf.abs().transpose(-1, -2))
+    ds = p * rate * (dp - D)
+    off = p * rate * ((2 * 2.0 ** -8 + 2 * eps + rr) * (dp.abs() + D.abs()) + off_d)
+
+    def shared(x):
+        return x.view(x.shape[0], Hk, H // Hk, *x.shape[2:]).sum(2)
+
+    def up(ref, err, terms):
+        err = err + 2.0 ** -14 * terms
+        return ref, err + 2.0 ** -8 * (ref.abs() + err) + tiny
+
+    dst, offt, pt = (x.transpose(-1, -2) for x in (ds, off, p))
+    dq = up(ds @ kf * scale, off @ kf.abs() * scale, ds.abs() @ kf.abs() * scale)
+    dk = up(shared(dst @ qf) * scale, shared(offt @ qf.abs()) * scale, shared(dst.abs() @ qf.abs()) * scale)
+    dv = up(shared(pt @ g), shared((2.0 ** -8 + 2 * eps.transpose(-1, -2)) * pt @ g.abs()), shared(pt @ g.abs()))
+    return (o, off_o), (lse, eps[..., 0] + 2.0 ** -20 * lse.abs()), dq, dk, dv
+
+
+@pytest.mark.parametrize("cap,mult", [(1e-3, 1.0), (0.25, 3.0), (1.0, 30.0), (30.0, 300.0), (1000.0, 3.0), (1000.0, 3000.0)])
+@pytest.mark.parametrize("d,bias", [(32, True), (64, False), (128, False), (128, True)])
+def test_scores_beyond_the_cap(fa_lib, d, bias, cap, mult):
+    """Caps at both ends, scores from a small part of the cap to thousands of it, signs of both kinds.  Where all scores of a
+    row are far beyond it, its gradients are as small as the cap's derivative."""
+    fa = fa_lib
+    B, H, Hk, N = 2, 4, 2, 300
+    g = torch.Generator().manual_seed(23)
+    q, k, v, do = (rand(g, B, h, N, d, mult=x) for h, x in ((H, mult), (Hk, 1.0), (Hk, 1.0), (H, 1.0)))
+    slopes = torch.rand(H, generator=g).to(DEV) * 0.1 if bias else None
+    m = fa.mask_ranges(B, N, causal=True, documents=i32([[0, 100, 300], [0, 250, 290]]))
+    o, lse = fa.attention_ranges(q, k, v, m, softcap=cap, slopes=slopes)
+    got = (o, lse, *fa.attention_ranges_backward(q, k, v, o, lse, do, m, softcap=cap, slopes=slopes))
+    for x, (ref, tol), name in zip(got, capped_reference(q, k, v, do, m, d ** -0.5, cap, slopes), ("O", "L", "dQ", "dK", "dV")):
+        close(x, ref, tol, name)
+    clean_status(fa)
+
+
+# ------------------------------------------------------------------ masks
+
+@pytest.mark.parametrize("d,cap,mult", [(64, 0.0, 4.0), (128, 300.0, 3.0)])
+@pytest.mark.parametrize("Nq,Nk", [(2500, 1100), (1200, 3000)])
+def test_ranges_far_from_their_rows(fa_lib, d, cap, mult, Nq, Nk):
+    """Ranges that run against the rows' order, more rows than keys, with slopes either way: biases of hundreds, on either
+    side of the row's position, in tiles that one row of many sees.  A bias is off by 2^-22 of it, which is less than what
+    the products' bound of 2^-16 size leaves beyond the error of a sum of 128 (2^-17 size)."""
+    fa = fa_lib
+    H, Hk = 4, 2
+    g = torch.Generator().manual_seed(29)
+    q, k, v, do = (rand(g, 1, h, n, d, mult=x) for h, n, x in ((H, Nq, mult), (Hk, Nk, mult), (Hk, Nk, 1.0), (H, Nq, 1.0)))
+    i = torch.arange(Nq)
+    first = (Nk - 1 - i * Nk // Nq - torch.randint(0, 200, (Nq,), generator=g)).clamp_min(0)
+    last = (first + torch.randint(0, 300, (Nq,), generator=g)).clamp_max(Nk)
+    last[::97] = Nk
+    m = fa.range_mask(first[None].int().to(DEV), last[None].int().to(DEV), Nk)
+    slopes = torch.tensor([0.2, 0.05, -0.0125, -0.2], device=DEV)
+    size = orc.forward(q, k, v, m.first, m.last, d ** -0.5, cap, slopes)[3]
+    assert 32 * size[:, :, (first < last).to(DEV)].min() >= 0.2 * 3000
+    check(fa, q, k, v, m, cap, slopes, do=do)
