@@ -83,7 +83,7 @@ struct RCfg {
 };
 
 // A unit's keys whose values were taken out: bit r of a tile's words for its key r.  More tiles than kBadTiles: the
-// epilogue looks at every key of a row.
+// epilogue looks at every key that one of its rows sees.
 constexpr int kBadTiles = 8;
 struct BadKeys {
   int count;
@@ -343,19 +343,55 @@ FA_DEV void clean_tile(uint8_t* tile, int tile_index, BadKeys* bad, int lane) {
   fence_proxy_async_smem();  // the product reads what was written here
 }
 
-// Adds the values that are not finite, of a key, to a stored row of O.
+// What a row sees that is not finite, a bit an element: +infinity or NaN in pos, -infinity or NaN in neg.
 template <int D>
-FA_DEV void add_not_finite(const __nv_bfloat16* v, __nv_bfloat16* o) {
-#pragma unroll 1
-  for (int u = 0; u < D / 2; ++u) {
-    const uint32_t x = reinterpret_cast<const uint32_t*>(v)[u], f = not_finite(x);
-    if (f) {
-      uint32_t* at = reinterpret_cast<uint32_t*>(o) + u;
-      const uint32_t keep = x & ((f >> 15) * 0xffffu), y = *at;
-      *at = pack_bf16x2(__uint_as_float(y << 16) + __uint_as_float(keep << 16),
-                        __uint_as_float(y & 0xffff0000u) + __uint_as_float(keep & 0xffff0000u));
-    }
+struct NotFinite {
+  uint32_t pos[D / 32], neg[D / 32];
+};
+
+// A key's values (the whole warp), noted for the lanes whose row sees it.
+template <int D>
+FA_DEV void note_key(NotFinite<D>& nf, const __nv_bfloat16* v, bool sees, int lane) {
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) {
+    const uint32_t x = reinterpret_cast<const uint16_t*>(v)[32 * i + lane];
+    const bool f = (x & 0x7f80u) == 0x7f80u, nan = (x & 0x7fu) != 0, minus = x >> 15 != 0;
+    const uint32_t p = __ballot_sync(0xffffffffu, f && (nan || !minus)), n = __ballot_sync(0xffffffffu, f && (nan || minus));
+    if (sees) nf.pos[i] |= p, nf.neg[i] |= n;
   }
+}
+
+// Which of eight keys hold a value that is not finite (the whole warp, D / 32 elements a lane; keys behind hi do not).
+template <int D>
+FA_DEV uint32_t look_at_8(const __nv_bfloat16* v, long long stride, int j0, int hi, int lane) {
+  constexpr int W = D == 128 ? 2 : 1;
+  uint32_t x[8][W], keys = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const __nv_bfloat16* at = v + min(j0 + e, hi - 1) * stride + D / 32 * lane;
+#pragma unroll
+    for (int w = 0; w < W; ++w)
+      x[e][w] = D == 32 ? *reinterpret_cast<const uint16_t*>(at) : reinterpret_cast<const uint32_t*>(at)[w];
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (__any_sync(0xffffffffu, (not_finite(x[e][0]) | not_finite(x[e][W - 1])) != 0)) keys |= 1u << e;
+  return j0 + 8 <= hi ? keys : keys & ((1u << (hi - j0)) - 1u);
+}
+
+// Adds what was noted to a stored row of O.
+template <int D>
+FA_DEV void add_not_finite(const NotFinite<D>& nf, __nv_bfloat16* o) {
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i)
+#pragma unroll 1
+    for (uint32_t any = nf.pos[i] | nf.neg[i]; any != 0; any &= any - 1) {
+      const int e = __ffs(any) - 1;
+      const bool p = nf.pos[i] >> e & 1u, n = nf.neg[i] >> e & 1u;
+      __nv_bfloat16* at = o + 32 * i + e;
+      if (p && n) *reinterpret_cast<uint16_t*>(at) = 0x7fff;
+      else *at = __float2bfloat16(__bfloat162float(*at) + (p ? INFINITY : -INFINITY));
+    }
 }
 
 template <int D, int MOD>
@@ -762,16 +798,23 @@ __global__ void __launch_bounds__(RCfg<D>::NTHREADS, 1)
           const BadKeys& bad = bad_keys[slot];
           const int n_bad = bad.count;
           const __nv_bfloat16* v = a.V + b * a.sv.b + h / a.G * a.sv.h;
-          __nv_bfloat16* orow = a.O + (row0 + q) * D;
+          NotFinite<D> nf{};
+          // The listed keys, or all that a row of the warp sees, eight at a time.  (Each lane by itself, key by key and into
+          // memory took 15 us a key of the longest row: 122 ms where it sees 8192.)
           const bool listed = n_bad <= kBadTiles;
-          if (q < m.Nq) {
+          const int hi = listed ? 4 * n_bad : __reduce_max_sync(0xffffffffu, last);
+          const int step = listed ? 1 : 8;
 #pragma unroll 1
-            for (int i = 0; i < (listed ? n_bad * C::BN : last - first); ++i) {
-              const int t = i / C::BN, r = i % C::BN, j = listed ? bad.tile[t] * C::BN + r : first + i;
-              if (j >= first && j < last && (!listed || (bad.words[t][r >> 5] >> (r & 31) & 1u)))
-                add_not_finite<D>(v + j * a.sv.n, orow);
+          for (int i = listed ? 0 : __reduce_min_sync(0xffffffffu, first < last ? first : INT_MAX); i < hi; i += step) {
+            uint32_t keys = listed ? bad.words[i >> 2][i & 3] : look_at_8<D>(v, a.sv.n, i, hi, lane);
+            const int j0 = listed ? bad.tile[i >> 2] * C::BN + 32 * (i & 3) : i;
+#pragma unroll 1
+            for (; keys != 0; keys &= keys - 1) {
+              const int j = j0 + __ffs(keys) - 1;
+              note_key<D>(nf, v + j * a.sv.n, j >= first && j < last, lane);
             }
           }
+          if (q < m.Nq) add_not_finite<D>(nf, a.O + (row0 + q) * D);
         }
         mbar_arrive(bar(C::B_EFREE + slot));
         ++k;

@@ -1,5 +1,6 @@
 """Attention over ranges of keys at the limits of what it takes: keys that are not finite in the gradients, no
-query heads, scores far beyond the cap, masks far from their rows.
+query heads, scores far beyond the cap, masks far from their rows, many
+values that are not finite.
 
 Bounds as in test_gpu_o_ranges.py and oracle/ranges.py.
 """
@@ -193,3 +194,40 @@ def test_ranges_far_from_their_rows(fa_lib, d, cap, mult, Nq, Nk):
     size = orc.forward(q, k, v, m.first, m.last, d ** -0.5, cap, slopes)[3]
     assert 32 * size[:, :, (first < last).to(DEV)].min() >= 0.2 * 3000
     check(fa, q, k, v, m, cap, slopes, do=do)
+
+
+# ------------------------------------------------------------------ many values that are not finite
+
+@pytest.mark.parametrize("d,H,Nq,Nk,every", [(32, 2, 200, 3000, 7), (64, 2, 300, 2999, 1), (128, 2, 129, 3001, 31),
+                                              (128, 512, 128, 160000, 300), (64, 512, 128, 160000, 1)])
+def test_many_values_that_are_not_finite(fa_lib, d, H, Nq, Nk, every):
+    """In every tile that a unit takes with masked places, for several units of a CTA: each row's elements are infinite or NaN
+    by the keys it sees, the others as if those values were zeros, and no wait runs out."""
+    fa = fa_lib
+    g = torch.Generator().manual_seed(37)
+    q, k, v = rand(g, 1, H, Nq, d), rand(g, 1, 1, Nk, d), rand(g, 1, 1, Nk, d)
+    first = torch.randint(0, Nk // 2, (1, Nq), generator=g, dtype=torch.int32)
+    last = first + torch.randint(0, Nk // 2, (1, Nq), generator=g, dtype=torch.int32)
+    first[0, 0], last[0, 0] = 0, Nk
+    last[0, 1::64] = 0  # rows without keys: no tile is seen whole
+    m = fa.range_mask(first.to(DEV), last.to(DEV), Nk)
+    values = torch.tensor([INF, -INF, NAN], dtype=torch.bfloat16)
+    at = torch.arange(3, Nk, every)
+    what, e = torch.randint(0, 3, at.shape, generator=g), torch.randint(0, d // 2, at.shape, generator=g)
+    bad, zero = v.clone(), v.clone()
+    bad[0, 0, at.to(DEV), e.to(DEV)] = values[what].to(DEV)
+    zero[0, 0, at.to(DEV), e.to(DEV)] = 0.0
+    want, wl = fa.attention_ranges(q, k, zero, m)
+    o, lse = fa.attention_ranges(q, k, bad, m)
+    clean_status(fa)
+    assert torch.equal(lse, wl)
+
+    def sees(some):  # [Nq, d]: whether the row sees a key with such an element
+        n = torch.cat([torch.zeros(1, d), (some.float().cumsum(0))]).double()
+        return n[m.last[0].cpu().long()] - n[m.first[0].cpu().long()] > 0
+
+    x = bad[0, 0].cpu()
+    up, down = sees((x == INF) | torch.isnan(x)), sees((x == -INF) | torch.isnan(x))
+    add = torch.where(up & down, NAN, torch.where(up, INF, torch.where(down, -INF, 0.0))).to(DEV)
+    ref = want.double() + add
+    close(o, ref, torch.zeros_like(ref), "O")
