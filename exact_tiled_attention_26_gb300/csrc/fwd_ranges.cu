@@ -32,6 +32,15 @@
 namespace fa {
 namespace {
 
+// Long rows (LONG, with more than kLongKeys keys).  The tensor cores cut what they add below 2^-25 of the sum, so a sum of
+// n like terms is off by up to n 2^-26: with equal weights 0.5 % at 2^20 keys, 33 % at 2^26.  There O is added to a sum of
+// its own in fp32 every kSegment key tiles, as are the weights' sums; its columns were the third S buffer's.  2048 rows of
+// some 2^18 keys, 8 + 2 heads, d = 128: 1.98 ms, with three buffers 1.75; d = 64 1.87 and 1.76; capped 2.90 and 2.78.
+constexpr int kLongKeys = 1 << 18, kSegment = 512;
+struct SegmentSums {
+  float l = 0.f, lr = 0.f;  // of the segments before this one, as SoftmaxRow's
+};
+
 constexpr int kAgain = 1024;
 // A unit as the producer hands it to the other roles.  n: key tiles; kPassEnd: all units have been handed out once; kEnd:
 // no more.
@@ -45,7 +54,7 @@ struct __align__(16) Unit {
   int first[kRangeTile], last[kRangeTile];  // the rows' keys
 };
 
-template <int D>
+template <int D, bool LONG = false>
 struct RCfg {
   static constexpr int BM = kRangeTile, BN = kRangeTile;
   static constexpr int SWB = (D * 2 >= 128) ? 128 : D * 2;
@@ -56,7 +65,7 @@ struct RCfg {
   static constexpr int OFF_K = 2 * TILE;  // two stages
   static constexpr int OFF_V = OFF_K + 2 * TILE;
   static constexpr int OFF_BAR = OFF_V + 2 * TILE;
-  static constexpr int NSB = 3;  // S buffers
+  static constexpr int NSB = LONG ? 2 : 3;  // S buffers
   static constexpr int B_QFULL = 0, B_QEMPTY = 2, B_KFULL = 4, B_KEMPTY = 6, B_VFULL = 8, B_VEMPTY = 10, B_VCLEAN = 12,
                        B_SFULL = 14, B_PFULL = 17, B_PFREE = 20, B_OFULL = 23, B_OFREE = 24, B_SDONE = 25, B_PVDONE = 26,
                        B_EREADY = 27,  // [unit parity] row state of the unit written by the softmax warps
@@ -77,8 +86,8 @@ struct RCfg {
   static constexpr int OFF_TOPS = OFF_ROWS + 2 * 5 * BM * 4;  // [tile parity][half][128] floats
   static constexpr int SMEM_USED = OFF_TOPS + 2 * 2 * BM * 4;
   static constexpr int SMEM = (SMEM_USED + 1024 > 120 * 1024) ? SMEM_USED + 1024 : 120 * 1024;
-  static constexpr int TM_S0 = 0, TM_O = NSB * 128, TM_COLS = 512;
-  static_assert(TM_O + D <= TM_COLS, "tensor memory budget");
+  static constexpr int TM_S0 = 0, TM_O = NSB * 128, TM_SUM = TM_O + 128, TM_COLS = 512;
+  static_assert((LONG ? TM_SUM : TM_O) + D <= TM_COLS, "tensor memory budget");
   static_assert(SMEM <= 232448, "shared memory budget");
 };
 
@@ -169,25 +178,21 @@ FA_DEV void keep_seen64(float (&s)[64], const uint32_t (&see)[2]) {
     if (!(see[k >> 5] >> (k & 31) & 1u)) s[k] = -INFINITY;
 }
 
-// Half a key tile (64 keys) for the calling thread's query row: S at tS becomes P = 2^(score - reference) in bf16 over its
-// first 32 columns.  The reference is moved lazily as in fwd_softmax.cuh; both halves of a row have the same, as they
-// exchange their largest score of every tile (`top`: from this half's to the row's, false: gave up) and each rescales its
-// own columns of O.  lo, hi: the row's keys, relative to the half (masked tiles only); dist0: the row's position minus the
-// half's first key; side: +1 where all keys of the tile are at or before all its rows, -1 behind them, 0 on both sides.
-// Moves the row's reference for a tile whose largest score is m_tile, where that has to be.
-template <int D, class WaitO>
-FA_DEV bool move_reference(SoftmaxRow& st, float m_tile, bool first, uint32_t tO, int half, WaitO&& wait_o) {
-  if (first) {
+// Moves the row's reference for a tile whose largest score is m_tile, where that has to be.  j: the unit's tile.
+template <int D, bool LONG, class WaitO>
+FA_DEV bool move_reference(SoftmaxRow& st, SegmentSums& sums, float m_tile, int j, uint32_t tO, int half, WaitO&& wait_o) {
+  if (j == 0) {
     st.m_run = m_tile + kFwdMaxHeadroom;  // -inf stays -inf (no key seen so far)
     return true;
   }
-  const bool move = m_tile > st.m_run + kFwdRescaleThreshold;
-  if (!__any_sync(0xffffffffu, move)) return true;
+  const bool move = m_tile > st.m_run + kFwdRescaleThreshold, take = LONG && j % kSegment == 0;
+  if (!take && !__any_sync(0xffffffffu, move)) return true;
   const float m_new = m_tile + kFwdMaxHeadroom;
   const float alpha = move ? ex2(st.m_run - m_new) : 1.f;
   if (move) {
     st.l_run *= alpha;
     st.lr_run *= alpha;
+    if (LONG) sums.l *= alpha, sums.lr *= alpha;
     st.m_run = m_new;
   }
   if (!wait_o()) return false;
@@ -199,18 +204,36 @@ FA_DEV bool move_reference(SoftmaxRow& st, float m_tile, bool first, uint32_t tO
     tmem_ld_wait<16>(o);
 #pragma unroll
     for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-    tmem_st16(tO + 16 * c, o);
+    if (LONG && j > kSegment) {  // there are segments before this one
+      uint32_t x[16];
+      const uint32_t tX = tO + (RCfg<D, LONG>::TM_SUM - RCfg<D, LONG>::TM_O) + 16 * c;
+      tmem_ld16(tX, x);
+      tmem_ld_wait<16>(x);
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        x[i] = __float_as_uint(fmaf(__uint_as_float(x[i]), alpha, take ? __uint_as_float(o[i]) : 0.f));
+      tmem_st16(tX, x);
+    } else if (take) {
+      tmem_st16(tO + (RCfg<D, LONG>::TM_SUM - RCfg<D, LONG>::TM_O) + 16 * c, o);
+    }
+    if (!take) tmem_st16(tO + 16 * c, o);  // (else the next product overwrites it)
   }
   tmem_st_wait();
+  if (take) sums.l += st.l_run, sums.lr += st.lr_run, st.l_run = 0.f, st.lr_run = 0.f;
   return true;
 }
 
-template <int D, int MOD, class Top, class WaitO>
-FA_DEV bool ranges_half(SoftmaxRow& st, uint32_t tS, uint32_t tO, int half, bool first, bool masked, int lo, int hi,
-                        int dist0, int side, const ScoreMod& mod, float slope, Top&& top, WaitO&& wait_o) {
+// Half a key tile (64 keys) for the calling thread's query row: S at tS becomes P = 2^(score - reference) in bf16 over its
+// first 32 columns.  The reference is moved lazily as in fwd_softmax.cuh; both halves of a row have the same, as they
+// exchange their largest score of every tile (`top`: from this half's to the row's, false: gave up) and each rescales its
+// own columns of O.  lo, hi: the row's keys, relative to the half (masked tiles only); dist0: the row's position minus the
+// half's first key; side: +1 where all keys of the tile are at or before all its rows, -1 behind them, 0 on both sides.
+template <int D, int MOD, bool LONG, class Top, class WaitO>
+FA_DEV bool ranges_half(SoftmaxRow& st, SegmentSums& sums, uint32_t tS, uint32_t tO, int half, int j, bool masked, int lo,
+                        int hi, int dist0, int side, const ScoreMod& mod, float slope, Top&& top, WaitO&& wait_o) {
   if (masked && !__any_sync(0xffffffffu, lo < hi && hi > 0 && lo < 64)) {  // the warp has no pair here
     float m_tile = -INFINITY;
-    if (!top(&m_tile) || !move_reference<D>(st, m_tile, first, tO, half, wait_o)) return false;
+    if (!top(&m_tile) || !move_reference<D, LONG>(st, sums, m_tile, j, tO, half, wait_o)) return false;
     uint32_t p[16];
 #pragma unroll
     for (int k = 0; k < 16; ++k) p[k] = 0u;
@@ -268,7 +291,7 @@ FA_DEV bool ranges_half(SoftmaxRow& st, uint32_t tS, uint32_t tO, int half, bool
   }
   const float mx = fmaxf(fmax3(m4[0], m4[1], m4[2]), m4[3]);
   float m_tile = MOD == kModNone ? mx * mod.c_log2 : mx + base;
-  if (!top(&m_tile) || !move_reference<D>(st, m_tile, first, tO, half, wait_o)) return false;
+  if (!top(&m_tile) || !move_reference<D, LONG>(st, sums, m_tile, j, tO, half, wait_o)) return false;
   const float neg_m = st.m_run == -INFINITY ? 0.f : base - st.m_run;
   const uint64_t cc2 = f2pack(mod.c_log2, mod.c_log2), nm2 = f2pack(neg_m, neg_m);
   uint64_t ls[2] = {f2pack(0.f, 0.f), f2pack(0.f, 0.f)};
@@ -394,11 +417,11 @@ FA_DEV void add_not_finite(const NotFinite<D>& nf, __nv_bfloat16* o) {
     }
 }
 
-template <int D, int MOD>
-__global__ void __launch_bounds__(RCfg<D>::NTHREADS, 1)
+template <int D, int MOD, bool LONG>
+__global__ void __launch_bounds__(RCfg<D, LONG>::NTHREADS, 1)
     fwd_ranges_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV, const __grid_constant__ FwdRangesArgs a) {
-  using C = RCfg<D>;
+  using C = RCfg<D, LONG>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
   const uint32_t sb = smem_u32(smem);
@@ -621,7 +644,8 @@ __global__ void __launch_bounds__(RCfg<D>::NTHREADS, 1)
           for (int c = 0; c < 2; ++c) {
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
-              mma_ts(tmem + C::TM_O, aP + 64 * c + 8 * ks, desc_at(vd, mnmajor_off<C::SWB>(ks)), idO, j > 0 || c > 0 || ks > 0);
+              mma_ts(tmem + C::TM_O, aP + 64 * c + 8 * ks, desc_at(vd, mnmajor_off<C::SWB>(ks)), idO,
+                     (LONG ? j % kSegment != 0 : j > 0) || c > 0 || ks > 0);
             vd = desc_at(vd, mnmajor_off<C::SWB>(4));
           }
           mma_commit(bar(C::B_VEMPTY + s));
@@ -682,6 +706,7 @@ __global__ void __launch_bounds__(RCfg<D>::NTHREADS, 1)
         if (u == nullptr) break;
         const int n = u->n, slot = k & 1;
         SoftmaxRow st;
+        SegmentSums sums;
         for (int j = 0; j < n; ++j, ++kv) {
           const int b = kv % C::NSB, k0 = (u->lo + j) * C::BN, p0 = u->qt * C::BM + m.Nk - m.Nq;
           if (!(ok = mbar_wait_warp(bar(C::B_SFULL + b), (kv / C::NSB) & 1, guard, SITE_R_SOFTMAX))) break;
@@ -711,7 +736,8 @@ __global__ void __launch_bounds__(RCfg<D>::NTHREADS, 1)
             lo = u->first[row] - c0, hi = u->last[row] - c0;
             masked = !__all_sync(0xffffffffu, lo <= 0 && hi >= 64);
           }
-          ok = ranges_half<D, MOD>(st, tS, tO, half, j == 0, masked, lo, hi, p0 + row - c0, side, a.mod, slope, top, wait_o);
+          ok = ranges_half<D, MOD, LONG>(st, sums, tS, tO, half, j, masked, lo, hi, p0 + row - c0, side, a.mod, slope, top,
+                                         wait_o);
           if (!ok) break;
           tc_fence_before();
           mbar_arrive(bar(C::B_PFULL + b));
@@ -722,8 +748,8 @@ __global__ void __launch_bounds__(RCfg<D>::NTHREADS, 1)
         if (k >= 2 && !(ok = mbar_wait_warp(bar(C::B_EFREE + slot), ((k >> 1) & 1) ^ 1, guard, SITE_R_SOFTMAX))) break;
         float* rs = rows + slot * 5 * C::BM;
         if (half == 0) rs[row] = st.m_run;
-        rs[(1 + 2 * half) * C::BM + row] = st.l_run;
-        rs[(2 + 2 * half) * C::BM + row] = st.lr_run;
+        rs[(1 + 2 * half) * C::BM + row] = LONG ? sums.l + st.l_run : st.l_run;
+        rs[(2 + 2 * half) * C::BM + row] = LONG ? sums.lr + st.lr_run : st.lr_run;
         mbar_arrive(bar(C::B_EREADY + slot));
       }
     }
@@ -768,6 +794,13 @@ __global__ void __launch_bounds__(RCfg<D>::NTHREADS, 1)
             uint32_t o[32];
             tmem_ld32(tl + C::TM_O + 32 * c, o);
             tmem_ld_wait<32>(o);
+            if (LONG && n > kSegment) {
+              uint32_t x[32];
+              tmem_ld32(tl + C::TM_SUM + 32 * c, x);
+              tmem_ld_wait<32>(x);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) + __uint_as_float(x[i]));
+            }
             if (c == D / 32 - 1) {
               tc_fence_before();
               mbar_arrive(bar(C::B_OFREE));  // the next unit's first P V may overwrite O
@@ -846,9 +879,10 @@ int heads_at_once(const RangesLaunch& a) {
   return G * static_cast<int>(n < 1 ? 1 : n > a.Hk ? a.Hk : n);
 }
 
-template <int D, int MOD>
+template <int D, int MOD, bool LONG = false>
 fa_status launch(const RangesLaunch& a) {
-  using C = RCfg<D>;
+  if (!LONG && a.Nk > kLongKeys) return launch<D, MOD, true>(a);
+  using C = RCfg<D, LONG>;
   int dev = 0, nsm = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return FA_ERR_CUDA;
@@ -859,7 +893,7 @@ fa_status launch(const RangesLaunch& a) {
                     !encode_bf16_rows(&mV, a.V, D, a.Nk, a.Hk, a.B, a.sv, C::CE, C::BN))))
     return FA_ERR_CUDA;
   if (a.Nk == 0) mK = mV = mQ;
-  auto kern = fwd_ranges_kernel<D, MOD>;
+  auto kern = fwd_ranges_kernel<D, MOD, LONG>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
     return FA_ERR_CUDA;
   const long long units = static_cast<long long>(a.B) * a.mask.Tq * a.H;

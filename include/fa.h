@@ -436,7 +436,8 @@ fa_status fa_fwd_ranges(const void* Q, const void* K, const void* V, void* O, fl
  * rows see makes its dK and dV and those rows' dQ NaN (and, where L is NaN, the gradients of
  * what these rows see).  (An infinity or NaN in a row of Q or dO, or in a value, that takes part
  * makes gradients NaN, also of keys and rows near it that it does not see.)  dQ's sums over key tiles are fp32 additions in no fixed order; dK and dV are the
- * same on every run.  Slopes are constants: they have no gradient.
+ * same on every run.  They add up in the tensor cores, which cut each term below 2^-25 of the
+ * sum: n terms (rows times query heads) of one sign and size are off by up to n 2^-26 of it.  Slopes are constants: they have no gradient.
  */
 size_t fa_bwd_ranges_workspace_size(int B, int H, int Hk, int Nq, int Nk, int d);
 fa_status fa_bwd_ranges(const void* Q, const void* K, const void* V, const void* O, const void* dO, const float* L,

@@ -1,6 +1,6 @@
 """Attention over ranges of keys at the limits of what it takes: keys that are not finite in the gradients, no
 query heads, scores far beyond the cap, masks far from their rows, many
-values that are not finite.
+values that are not finite, rows of very many keys.
 
 Bounds as in test_gpu_o_ranges.py and oracle/ranges.py.
 """
@@ -10,7 +10,7 @@ import pytest
 import torch
 
 from oracle import ranges as orc
-from test_gpu_o_ranges import check, close, rand
+from test_gpu_o_ranges import check, check_forward, close, rand, slopes_of
 from test_gpu_q_ranges_edges import INF, NAN, clean_status, i32
 
 pytestmark = pytest.mark.gpu
@@ -199,7 +199,8 @@ def test_ranges_far_from_their_rows(fa_lib, d, cap, mult, Nq, Nk):
 # ------------------------------------------------------------------ many values that are not finite
 
 @pytest.mark.parametrize("d,H,Nq,Nk,every", [(32, 2, 200, 3000, 7), (64, 2, 300, 2999, 1), (128, 2, 129, 3001, 31),
-                                              (128, 512, 128, 160000, 300), (64, 512, 128, 160000, 1)])
+                                              (128, 512, 128, 160000, 300), (64, 512, 128, 160000, 1),
+                                              (128, 3, 100, 300000, 300), (32, 3, 200, 270000, 77)])
 def test_many_values_that_are_not_finite(fa_lib, d, H, Nq, Nk, every):
     """In every tile that a unit takes with masked places, for several units of a CTA: each row's elements are infinite or NaN
     by the keys it sees, the others as if those values were zeros, and no wait runs out."""
@@ -231,3 +232,45 @@ def test_many_values_that_are_not_finite(fa_lib, d, H, Nq, Nk, every):
     add = torch.where(up & down, NAN, torch.where(up, INF, torch.where(down, -INF, 0.0))).to(DEV)
     ref = want.double() + add
     close(o, ref, torch.zeros_like(ref), "O")
+
+
+# ------------------------------------------------------------------ rows of very many keys
+
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("n", [1 << 18, (1 << 22) + 1000])
+def test_sums_of_very_many_like_terms(fa_lib, d, n):
+    """Equal weights, values in 1 .. 2.  The tensor cores cut each term by up to 2^-25 of the sum; over 2^18 keys at most (2^16
+    where there are more) that is 2^-7 (2^-9) of it, and half of that on the average; the result's rounding 2^-8."""
+    fa = fa_lib
+    g = torch.Generator(device=DEV).manual_seed(41)
+    q = torch.zeros(1, 1, 100, d, dtype=torch.bfloat16, device=DEV)
+    v = (1 + torch.rand(1, 1, n, d, generator=g, device=DEV)).to(torch.bfloat16)
+    o, lse = fa.attention_ranges(q, v, v, fa.mask_ranges(1, 100, n))
+    ref = v.double().mean(2, keepdim=True)
+    close(o, ref.expand_as(o), ((2.0 ** -8 + (2.0 ** -8 if n == 1 << 18 else 2.0 ** -9)) * ref).expand_as(o), "O")
+    assert (lse - math.log(n)).abs().max() <= 2.0 ** -18 + 2.0 ** -20 * 16
+    clean_status(fa)
+
+
+@pytest.mark.parametrize("d,cap,bias", [(128, 0.0, False), (128, 20.0, True), (64, 0.0, True), (32, 20.0, False)])
+def test_long_rows(fa_lib, d, cap, bias):
+    """Rows of 2^18 keys and more: ranges that begin and end anywhere, rows without keys, scores that grow along the row
+    (references move, before and after a segment's end) or fall.  Slopes of 2^-10 at most: biases of 300, of which 2^-22 is
+    less than the products' bound leaves (2^-17 size, and size is 2.5 or more for d >= 32)."""
+    fa = fa_lib
+    H, Hk, Nq, Nk = 2, 1, 140, (1 << 18) + 70001
+    g = torch.Generator().manual_seed(43)
+    q, k, v = rand(g, 1, H, Nq, d, mult=1.5), rand(g, 1, Hk, Nk, d, mult=1.5), rand(g, 1, Hk, Nk, d)
+    k *= torch.linspace(0.3, 3.0, Nk, device=DEV)[:, None].to(torch.bfloat16)
+    first = torch.randint(0, Nk // 3, (1, Nq), generator=g, dtype=torch.int32)
+    last = Nk - torch.randint(0, Nk // 3, (1, Nq), generator=g, dtype=torch.int32)
+    first[0, 5:9], last[0, 5:9] = 0, Nk
+    last[0, 10::50] = 0
+    last[0, 11::50] = first[0, 11::50] + 70
+    m = fa.range_mask(first.to(DEV), last.to(DEV), Nk)
+    slopes = slopes_of(H) * 2.0 ** -6 if bias else None
+    o, lse = fa.attention_ranges(q, k, v, m, softcap=cap, slopes=slopes)
+    check_forward(o, lse, q, k, v, m, d ** -0.5, cap, slopes)
+    o2, lse2 = fa.attention_ranges(q, k, v, m, softcap=cap, slopes=slopes)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    clean_status(fa)
