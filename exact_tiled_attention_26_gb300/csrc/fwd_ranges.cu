@@ -42,6 +42,7 @@ struct SegmentSums {
 };
 
 constexpr int kAgain = 1024;
+constexpr uint64_t kTileLimitNs = 8000;  // what a tile pair may take at most, see the epilogue
 // A unit as the producer hands it to the other roles.  n: key tiles; kPassEnd: all units have been handed out once; kEnd:
 // no more.
 constexpr int kRing = 4, kPassEnd = -1, kEnd = -2;
@@ -777,7 +778,9 @@ __global__ void __launch_bounds__(RCfg<D, LONG>::NTHREADS, 1)
         const int slot = k & 1;
         float L = -INFINITY, l = 0.f, lr = 0.f, m_run = 0.f;
         if (n > 0) {
-          if (!(ok = mbar_wait_warp(bar(C::B_EREADY + slot), (k >> 1) & 1, guard, SITE_R_SOFTMAX))) break;
+          // the one wait that a whole unit's tiles are computed under (0.8 us each: 2^29 keys take 3.4 s)
+          const uint64_t limit = kWaitLimitNs + static_cast<uint64_t>(n) * kTileLimitNs;
+          if (!(ok = mbar_wait_warp(bar(C::B_EREADY + slot), (k >> 1) & 1, guard, SITE_R_SOFTMAX, limit))) break;
           const float* rs = rows + slot * 5 * C::BM;
           m_run = rs[row], l = rs[C::BM + row] + rs[3 * C::BM + row], lr = rs[2 * C::BM + row] + rs[4 * C::BM + row];
           if (!(ok = mbar_wait_warp(bar(C::B_OFULL), k & 1, guard, SITE_R_SOFTMAX))) break;

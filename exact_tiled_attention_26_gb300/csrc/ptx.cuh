@@ -76,8 +76,9 @@ FA_DEV bool mbar_wait(uint32_t bar, uint32_t parity, const Guard& g, int site,
 
 // Same, taken by a whole warp: the result is uniform across the warp so that
 // warp-collective instructions that follow are executed by all lanes or none.
-FA_DEV bool mbar_wait_warp(uint32_t bar, uint32_t parity, const Guard& g, int site) {
-  const bool ok = mbar_wait(bar, parity, g, site);
+FA_DEV bool mbar_wait_warp(uint32_t bar, uint32_t parity, const Guard& g, int site,
+                           uint64_t limit_ns = kWaitLimitNs) {
+  const bool ok = mbar_wait(bar, parity, g, site, limit_ns);
   return __all_sync(0xffffffffu, ok);
 }
 

@@ -274,3 +274,19 @@ def test_long_rows(fa_lib, d, cap, bias):
     o2, lse2 = fa.attention_ranges(q, k, v, m, softcap=cap, slopes=slopes)
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
     clean_status(fa)
+
+
+def test_a_row_of_very_many_keys(fa_lib):
+    """One unit of 2^22 tiles and one more takes longer than any single wait may.  All scores are 0 and all values 1 (keys and
+    values are one tensor): weights are a power of two, and the sums, below 2^6 in steps of 2^-17, exact but for the last
+    tile's 77 weights of 2^-24."""
+    fa = fa_lib
+    n = (1 << 29) + 77
+    if torch.cuda.mem_get_info()[0] < 64 * n + (4 << 30):
+        pytest.skip("not enough memory free")
+    q = torch.zeros(1, 1, 1, 32, dtype=torch.bfloat16, device=DEV)
+    k = torch.ones(1, 1, n, 32, dtype=torch.bfloat16, device=DEV)
+    m = fa.mask_ranges(1, 1, n)
+    o, lse = fa.attention_ranges(q, k, k, m)
+    clean_status(fa)
+    assert (o == 1).all() and abs(lse.item() - math.log(n)) <= 2.0 ** -18 + 2.0 ** -20 * 21
