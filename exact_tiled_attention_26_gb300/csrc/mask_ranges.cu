@@ -287,6 +287,8 @@ __global__ void __launch_bounds__(1024) mask_few_kernel(const __grid_constant__ 
   }
 }
 
+constexpr int kMostDocs = 1 << 29;  // sums of two places among the borders fit 32 bits
+
 fa_status launch_mask(const MaskView& m, const RowRules& r, cudaStream_t s) {
   if (m.B == 0 || (m.Tq == 0 && m.Tk == 0)) return FA_OK;
   if (static_cast<long long>(m.B) * m.Tq <= kFewTiles && static_cast<long long>(m.B) * m.Tk <= kFewTiles)
@@ -325,13 +327,14 @@ size_t fa_mask_size(int B, int Nq, int Nk) {
 
 fa_status fa_mask_ranges(void* mask, size_t mask_bytes, int B, int Nq, int Nk, int causal, int window,
                          const int* documents, int docs, const int* prefix, fa_stream_t stream) {
+  if (documents == nullptr) docs = 0;
   if (window < 0 || docs < 0 || (window > 0 && !causal) || (prefix != nullptr && (!causal || window > 0)) ||
       (documents != nullptr && docs == 0) || !aligned(documents, 4) || !aligned(prefix, 4))
     return FA_ERR_INVALID_ARG;
   MaskView m;
   const fa_status st = mask_args(mask, mask_bytes, B, Nq, Nk, &m);
   if (st != FA_OK) return st;
-  if (Nq > Nk) return FA_ERR_UNSUPPORTED;
+  if (Nq > Nk || docs > kMostDocs) return FA_ERR_UNSUPPORTED;
   return launch_mask(m, RowRules{documents, prefix, nullptr, nullptr, docs, causal != 0, window}, stream);
 }
 

@@ -391,8 +391,8 @@ size_t fa_mask_size(int B, int Nq, int Nk);
  * p = i + Nk - Nq, as in fa_fwd_ex.
  *   documents : int32 [B, docs+1], ascending borders in 0 .. Nk: document c of sequence b is
  *               at positions documents[b][c] .. documents[b][c+1] - 1.  A row sees keys of its
- *               own document, and none if it is in no document.  NULL (docs ignored): one
- *               document of all positions.  (Borders that do not ascend give some range
+ *               own document, and none if it is in no document; docs <= 2^29.  NULL (docs ignored):
+ *               one document of all positions.  (Borders that do not ascend give some range
  *               within the sequence.)
  *   causal    : a row sees no key behind its position
  *   window    : 0, or w > 0 with causal: only the w keys up to its position
