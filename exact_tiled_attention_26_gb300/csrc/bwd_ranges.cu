@@ -788,6 +788,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     tc_fence_after();
     tmem_dealloc(x.tmem, TM_COLS);
   }
+  pdl_wait();  // a CTA that skipped its work has not waited: what follows may rely on the kernel before having ended
 }
 
 // D = rowsum(dO * O) of every row (0 where the row sees no key: its dO may be anything), and the row's dQ sums cleared.

@@ -1,6 +1,6 @@
 """Attention over ranges of keys at the limits of what it takes: keys that are not finite in the gradients, no
 query heads, scores far beyond the cap, masks far from their rows, many
-values that are not finite, rows of very many keys.
+values that are not finite, rows of very many keys, a device error pending.
 
 Bounds as in test_gpu_o_ranges.py and oracle/ranges.py.
 """
@@ -290,3 +290,35 @@ def test_a_row_of_very_many_keys(fa_lib):
     o, lse = fa.attention_ranges(q, k, k, m)
     clean_status(fa)
     assert (o == 1).all() and abs(lse.item() - math.log(n)) <= 2.0 ** -18 + 2.0 ** -20 * 21
+
+
+# ------------------------------------------------------------------ a device error pending
+
+def test_calls_while_a_device_error_is_pending(fa_lib):
+    """A wait that ran out sets the status word: calls behind it skip their work and leave the outputs, the workspace may be
+    used again as soon as they have ended, and once the error is taken results are right."""
+    fa = fa_lib
+    g = torch.Generator().manual_seed(47)
+    B, H, Hk, N, d = 2, 4, 2, 3000, 128
+    q, k, v, do = (rand(g, B, h, N, d) for h in (H, Hk, Hk, H))
+    m = fa.mask_ranges(B, N, causal=True)
+    o, lse = fa.attention_ranges(q, k, v, m)
+    want = fa.attention_ranges_backward(q, k, v, o, lse, do, m)
+    ws = torch.empty(fa.fa_bwd_ranges_workspace_size(B, H, Hk, N, N, d), dtype=torch.uint8, device=DEV)
+    outs = [torch.full_like(x, 7.0) for x in (q, k, v)]
+    stream = torch.cuda.current_stream().cuda_stream
+    fa.check(fa.fa_debug_timeout_probe(1000, stream))
+    for _ in range(20):
+        status = fa.fa_bwd_ranges(*(x.data_ptr() for x in (q, k, v, o, do, lse, *outs)), None, None, None, None,
+                                  m.buffer.data_ptr(), m.buffer.nbytes, B, H, Hk, N, N, d, 0.0, None, d ** -0.5,
+                                  ws.data_ptr(), ws.nbytes, stream)
+        assert status == 0
+        ws.fill_(0x5a)
+        assert (ws == 0x5a).all()
+    assert fa.fa_poll_device_error(stream)[0] == fa.FA_ERR_TIMEOUT
+    assert all((x == 7.0).all() for x in outs)
+    o2, lse2 = fa.attention_ranges(q, k, v, m)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    got = fa.attention_ranges_backward(q, k, v, o, lse, do, m, workspace=ws)
+    assert torch.equal(got[1], want[1]) and torch.equal(got[2], want[2])
+    clean_status(fa)
