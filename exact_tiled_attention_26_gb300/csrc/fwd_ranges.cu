@@ -418,6 +418,29 @@ FA_DEV void add_not_finite(const NotFinite<D>& nf, __nv_bfloat16* o) {
     }
 }
 
+// What a warp's rows see that is not finite, from a unit taken a second time: of the listed keys, or of all that one of the
+// rows sees, eight at a time.  (Each lane by itself, key by key and into memory took 15 us a key of the longest row: 122 ms
+// where it sees 8192.)  o: the lane's stored row, or null.  A function of its own: inlined, these rare lines made 16384
+// tokens take 1.54 ms instead of 1.51.
+template <int D>
+__device__ __noinline__ void take_not_finite(const BadKeys& bad, int n_bad, const __nv_bfloat16* v, long long stride,
+                                             int first, int last, __nv_bfloat16* o, int lane) {
+  NotFinite<D> nf{};
+  const bool listed = n_bad <= kBadTiles;
+  const int hi = listed ? 4 * n_bad : __reduce_max_sync(0xffffffffu, last), step = listed ? 1 : 8;
+#pragma unroll 1
+  for (int i = listed ? 0 : __reduce_min_sync(0xffffffffu, first < last ? first : INT_MAX); i < hi; i += step) {
+    uint32_t keys = listed ? bad.words[i >> 2][i & 3] : look_at_8<D>(v, stride, i, hi, lane);
+    const int j0 = listed ? bad.tile[i >> 2] * kRangeTile + 32 * (i & 3) : i;
+#pragma unroll 1
+    for (; keys != 0; keys &= keys - 1) {
+      const int j = j0 + __ffs(keys) - 1;
+      note_key<D>(nf, v + j * stride, j >= first && j < last, lane);
+    }
+  }
+  if (o != nullptr) add_not_finite<D>(nf, o);
+}
+
 template <int D, int MOD, bool LONG>
 __global__ void __launch_bounds__(RCfg<D, LONG>::NTHREADS, 1)
     fwd_ranges_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -834,23 +857,7 @@ __global__ void __launch_bounds__(RCfg<D, LONG>::NTHREADS, 1)
           const BadKeys& bad = bad_keys[slot];
           const int n_bad = bad.count;
           const __nv_bfloat16* v = a.V + b * a.sv.b + h / a.G * a.sv.h;
-          NotFinite<D> nf{};
-          // The listed keys, or all that a row of the warp sees, eight at a time.  (Each lane by itself, key by key and into
-          // memory took 15 us a key of the longest row: 122 ms where it sees 8192.)
-          const bool listed = n_bad <= kBadTiles;
-          const int hi = listed ? 4 * n_bad : __reduce_max_sync(0xffffffffu, last);
-          const int step = listed ? 1 : 8;
-#pragma unroll 1
-          for (int i = listed ? 0 : __reduce_min_sync(0xffffffffu, first < last ? first : INT_MAX); i < hi; i += step) {
-            uint32_t keys = listed ? bad.words[i >> 2][i & 3] : look_at_8<D>(v, a.sv.n, i, hi, lane);
-            const int j0 = listed ? bad.tile[i >> 2] * C::BN + 32 * (i & 3) : i;
-#pragma unroll 1
-            for (; keys != 0; keys &= keys - 1) {
-              const int j = j0 + __ffs(keys) - 1;
-              note_key<D>(nf, v + j * a.sv.n, j >= first && j < last, lane);
-            }
-          }
-          if (q < m.Nq) add_not_finite<D>(nf, a.O + (row0 + q) * D);
+          take_not_finite<D>(bad, n_bad, v, a.sv.n, first, last, q < m.Nq ? a.O + (row0 + q) * D : nullptr, lane);
         }
         mbar_arrive(bar(C::B_EFREE + slot));
         ++k;
