@@ -4,9 +4,10 @@
 //
 // A unit is a 128-key tile of a key head: K and V stay in shared memory while the CTA walks the query tiles of the
 // mask's table, for one query head of the key head after the other, and dK, dV add up in tensor memory over all of
-// them (over a part of the steps where a unit is split).  Roles, tensor-memory regions and the per-step barriers are those of bwd_steps.cuh; what is new is in the
-// element-wise step (row ranges, cap, bias) and in what its producer stages.  Persistent: one CTA per SM, units by the
-// mask's order, long ones in parts (split_places).  d = 32 runs with d = 64's tiles, whose second half the loads fill with zeros.
+// them (over a part of the steps where a unit is split).  Roles, tensor-memory regions and the per-step barriers are those
+// of bwd_steps.cuh; what is new is in the element-wise step (row ranges, cap, bias) and in what its producer stages.
+// Persistent: one CTA per SM, units by the mask's order, long ones in parts (split_places).  d = 32 runs with d = 64's
+// tiles, whose second half the loads fill with zeros (2 x 4096 tokens of documents, 16 + 4 heads: 108 us, d = 64 123).
 //
 // What no pair uses may hold anything: a query row that sees no key is zeroed in its tiles before the products with
 // dO and Q (their weights 0 would make NaN of a NaN), an infinite or NaN key is zeroed before dQ^T = K^T dS^T, and a
@@ -15,11 +16,11 @@
 //
 // Three launches: D and the cleared dQ sums; the products; dQ rounded to bf16, and split units' parts added.
 //
-// What bounds it.  Long rows (8192 tokens with a prefix, 32 + 8 heads, d = 128: 1.36 ms, 1025 TFLOP/s; 2.9 us a step): the
+// What bounds it.  Long rows (8192 tokens with a prefix, 32 + 8 heads, d = 128: 1.35 ms, 1035 TFLOP/s; 2.9 us a step): the
 // chain of a step, as in bwd_steps.cuh, and the reductions of dQ in L2.  The cap adds two operations of the
-// special-function unit an element (1.48 ms), the bias issue slots (1.37).  Short documents (2 x 4096 tokens, 16 + 4
-// heads: 168 us, capped 184): the fullest SM has 41 steps, with 29 on the average; 33 us are the first and the last
-// launch, which write and read the fp32 sums of dQ; and instruction fetches, as in fwd_ranges.cu (86 to 97 KB of code, of
+// special-function unit an element (1.49 ms), the bias issue slots (1.37).  Short documents (2 x 4096 tokens, 16 + 4
+// heads: 167 us, capped 185): the fullest SM has 41 steps, with 29 on the average; 33 us are the first and the last
+// launch, which write and read the fp32 sums of dQ; and instruction fetches, as in fwd_ranges.cu (86 to 99 KB of code, of
 // which some 31 run in every step: 16 more there made the 1.39 ms of an earlier form 1.71).
 #include <cmath>
 
@@ -67,7 +68,6 @@ constexpr int ROFF_STAGE = (ROFF_BAD + 2 * 4 * 4 + 15) / 16 * 16, RSMALL = ROFF_
 static_assert(RSMALL <= 3 * 1024 && sizeof(Stage) % 16 == 0, "small region");
 
 enum : int { SITE_RB_PRODUCER = 0x611, SITE_RB_MMA = 0x612, SITE_RB_COMPUTE = 0x613, SITE_RB_LAYOUT = 0x615 };
-enum : int { kModNone = 0, kModCap = 1, kModBias = 2 };
 
 struct BwdRangesArgs {
   MaskView m;
@@ -224,8 +224,6 @@ FA_DEV bool drain(const Ctx& x, int g, float* tile, int nq, int qw, int lane) {
   return true;
 }
 
-FA_DEV uint32_t not_finite(uint32_t x) { return ((x & 0x7f807f80u) + 0x00800080u) & 0x80008000u; }
-
 // A unit's K tile, looked through by the element-wise threads, each the row of its key: infinities and NaNs become zeros,
 // for the keys' part in dQ^T of rows that do not see them.  Returns what makes bf16 pairs NaN if the key is not finite,
 // else 0: the scores of such a key are not its own any more (S^T may have been made before or after), and the pairs that
@@ -288,10 +286,10 @@ FA_DEV void seen_pairs(const uint4* R4, uint32_t here, uint32_t (&see)[16]) {
 
 // A unit of more than 1.5 times the steps that an SM has on the average (and of 8 at least) is taken in kParts parts, each
 // with its share of the query tiles for all heads, whose sums the last kernel adds up.  There are fewer such units than
-// SMs.  (4096 tokens of packed documents, 4 key heads of 4 query heads each, 2 sequences: 49 steps instead of 41 on the
-// fullest SM, 29 on the average.)  Each CTA's pieces are as UnitWalk's, so that the CTAs stay at the same query heads at
-// a time: all of Q, dO and the sums of dQ may be more than L2.  Measured and not kept, main kernel: equal runs of steps per CTA whatever the units
-// (8192 tokens, 32 + 8 heads: 1.76 ms where whole units take 1.39); a queue, with long units split by query heads (4096
+// SMs.  (4096 tokens of packed documents, 4 key heads of 4 query heads each, 2 sequences: 41 steps on the fullest SM, 49
+// with whole units, 29 on the average.)  Pieces are dealt out to and fro as in UnitWalk, in the order of the key tiles'
+// work, so that the CTAs stay at the same query heads at a time: all of Q, dO and the sums of dQ may be more than L2.
+// Measured and not kept, main kernel: equal runs of steps per CTA whatever the units (8192 tokens, 32 + 8 heads: 1.76 ms where whole units take 1.39); a queue, with long units split by query heads (4096
 // tokens in one document: 475 us, 349).
 constexpr int kParts = 2;
 // How many key tiles of the mask's order are split.

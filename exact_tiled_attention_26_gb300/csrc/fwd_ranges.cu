@@ -18,12 +18,13 @@
 //
 // What bounds it.  Long rows (16384 tokens with a prefix, 32 + 8 heads, d = 128: 1.51 ms, 1475 TFLOP/s, 0.77 of a library
 // product's burst; 0.86 us a tile pair): issue of the two softmax warps of a scheduler, and shared memory's port, which
-// the products' operands and the loads share.  With one warp for a row's 128 scores the same took 1.71 ms.  With a cap the special-function unit (ranges_score.cuh), with
-// a bias the issue slots again (2.08 ms).  Short documents (2 x 4096 tokens, 7 documents each, 16 + 4 heads: 41.8 us, 25
-// of them the tile pairs at that rate): the units' borders, and instruction fetches.  The roles of a CTA run code of
-// their own all the time, and what does not fit the instruction caches comes from one that several SMs share: with 130 KB
-// of code its request rate was at 0.77 of its peak and the same call took 62 us.  So masked and whole tiles run
-// the same code, and what runs once a unit, and the issue of the products, is a loop.
+// the products' operands and the loads share.  With one warp for a row's 128 scores the same took 1.71 ms.  With a cap the
+// special-function unit (ranges_score.cuh), with a bias the issue slots again (2.07 ms).  Short documents (2 x 4096 tokens,
+// 7 documents each, 16 + 4 heads: 41.6 us, 25 of them the tile pairs at that rate): the units' borders, and instruction
+// fetches.  The roles of a CTA run code of their own all the time, and what does not fit the instruction caches comes from
+// one that several SMs share: with 130 KB of code its request rate was at 0.77 of its peak and the same call took 62 us
+// (now 70 KB).  So masked and whole tiles run the same code, and what runs once a unit, and the issue of the products, is a
+// loop.
 #include <type_traits>
 
 #include "fwd_softmax.cuh"
@@ -114,8 +115,6 @@ struct FwdRangesArgs {
   int H, G, group, qh, qb, kh, kb, vh, vb;  // (…h, …b: 0 where the tensor's heads, batches have stride 0)
   int* status;
 };
-
-enum : int { kModNone = 0, kModCap = 1, kModBias = 2 };  // bits of MOD
 
 // Whether all of a key tile is seen by all rows of the query tile.
 FA_DEV bool whole_tile(const volatile Unit& t, int k0) {
@@ -320,9 +319,6 @@ FA_DEV bool ranges_half(SoftmaxRow& st, SegmentSums& sums, uint32_t tS, uint32_t
   tmem_st_wait();
   return true;
 }
-
-// Bits of the halves of x that are infinite or NaN: bit 15 and bit 31.
-FA_DEV uint32_t not_finite(uint32_t x) { return ((x & 0x7f807f80u) + 0x00800080u) & 0x80008000u; }
 
 // A value tile with masked places (one warp): its infinities and NaNs become zeros, their keys go into `bad`.
 template <int D>

@@ -293,7 +293,8 @@ fa_status launch_mask(const MaskView& m, const RowRules& r, cudaStream_t s) {
   if (m.B == 0 || (m.Tq == 0 && m.Tk == 0)) return FA_OK;
   if (static_cast<long long>(m.B) * m.Tq <= kFewTiles && static_cast<long long>(m.B) * m.Tk <= kFewTiles)
     return launch_pdl(mask_few_kernel, dim3(1), dim3(1024), 0, s, m, r) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
-  if (m.Tq > 0 && launch_pdl(mask_rows_kernel, dim3((m.Tq + kRowWarps - 1) / kRowWarps, m.B), dim3(32 * kRowWarps), 0, s, m, r) != cudaSuccess)
+  if (m.Tq > 0 && launch_pdl(mask_rows_kernel, dim3((m.Tq + kRowWarps - 1) / kRowWarps, m.B), dim3(32 * kRowWarps), 0, s,
+                             m, r) != cudaSuccess)
     return FA_ERR_CUDA;
   if (m.Tk > 0 && launch_pdl(mask_keys_kernel, dim3((m.Tk + 63) / 64, m.B), dim3(256), 0, s, m) != cudaSuccess)
     return FA_ERR_CUDA;

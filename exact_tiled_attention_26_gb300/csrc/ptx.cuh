@@ -454,11 +454,14 @@ FA_DEV void warp_store_rows(uint32_t (&v)[N], uint8_t* base, size_t stride, int 
 // block until that kernel has completed and its memory writes are visible (a no-op
 // when the launch was an ordinary one).  pdl_trigger: let the next kernel on the
 // stream, if launched with launch_pdl, start now (its own pdl_wait still orders
-// its reads after this kernel's end).  Only the workspace clear triggers early: its
-// dependent, the backward kernel, has loads and products to do before it waits.
-// A dependent that could only wait (the dQ convert, the preprocess, the forward)
-// would hold SMs that another stream's kernels could use, so kernels followed by
-// one of those never trigger: their dependents start when they end.
+// its reads after this kernel's end).  The workspace clear and bwd_ranges_prepare
+// trigger early: their dependent, the backward kernel, has loads and products to do
+// before it waits.  So do the mask's first two kernels, which are short.  Other
+// dependents that could only wait (the dQ convert, the preprocess, the forward) would
+// hold SMs that another stream's kernels could use, so kernels followed by one of
+// those never trigger: their dependents start when they end.  What a dependent touches before its own pdl_wait
+// must have been written before the kernel that triggered waited itself: that one's
+// CTAs call pdl_wait first (bwd_ranges_prepare), or the dependent touches nothing.
 FA_DEV void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 FA_DEV void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 

@@ -39,8 +39,8 @@ struct KeyWork {
 };
 
 // The mask buffer (fa.h): row ranges, tile tables, the tiles of all sequences from the longest work down (as
-// b * tiles + tile; those without work last), and the key tiles' work.  Each part on 16 bytes.  Row i of sequence b sees keys first[b * Nq + i] <= j < last[b * Nq + i]
-// (both 0 for none).
+// b * tiles + tile; those without work last), and the key tiles' work.  Each part on 16 bytes.  Row i of sequence b sees
+// keys first[b * Nq + i] <= j < last[b * Nq + i] (both 0 for none).
 struct MaskView {
   int *first, *last;
   QueryTile* qt;  // [B, Tq]
@@ -92,6 +92,12 @@ struct UnitWalk {
     entry = order[place];
   }
 };
+
+// What a kernel does to the scores: bits of its MOD.
+enum : int { kModNone = 0, kModCap = 1, kModBias = 2 };
+
+// Bits of the halves of x that are infinite or NaN: bit 15 and bit 31.
+FA_DEV uint32_t not_finite(uint32_t x) { return ((x & 0x7f807f80u) + 0x00800080u) & 0x80008000u; }
 
 // Caps that are taken: a score's error is the cap's times some 2^-22 (ranges_score.cuh).
 constexpr float kCapMin = 1e-3f, kCapMax = 1e3f;

@@ -7,12 +7,12 @@ namespace fa {
 
 // cap tanh(s / cap) in base 2 for scores x before scaling (x = s / unit), made on the host.
 //   tanh(s / cap) = 1 - 2 / (1 + 2^y), y = 2 log2 e s / cap
-// in absolute error some 2^-22 whatever y is (2^y = infinity: 1; a NaN stays one).  Two operations of the special-function
-// unit an element, three with the weight's exponential: at 16 a clock and SM they take 3 x 1024 clocks for a tile's
-// 16384 scores, and bound a capped forward (16384 tokens, 32 + 8 heads, d = 128: 2.81 ms; uncapped 1.51).  So that takes one
-// reciprocal for four scores (cap_scores_fast, 2.41 ms).  The gradients and a decoded token are bound by other things and
-// are slower with it (8192 tokens: 1.51 ms against 1.48).  Measured besides for the forward: one reciprocal for two 2.64;
-// a polynomial of degree 13 where no score passes the cap 2.69, for every other pair of scores 2.48.
+// in absolute error some 2^-22 whatever y is (2^y = infinity: 1; a NaN stays one).  Two operations of the
+// special-function unit an element, three with the weight's exponential: at 16 a clock and SM they take 3 x 1024 clocks
+// for a tile's 16384 scores, and bound a capped forward (16384 tokens, 32 + 8 heads, d = 128: 2.81 ms; uncapped 1.51).
+// So that takes one reciprocal for four scores (cap_scores_fast, 2.40 ms).  The gradients and a decoded token are bound
+// by other things and were slower with it (8192 tokens: 1.51 ms against 1.48).  Measured besides for the forward: one
+// reciprocal for two 2.64; a polynomial of degree 13 where no score passes the cap 2.69, for every other pair 2.48.
 struct CapArgs {
   float cap_log2;  // cap log2 e; 0: no cap
   float to_y;      // y = x to_y

@@ -359,7 +359,7 @@ fa_status fa_fwd_tree(const void* Q, const fa_cache* cache, void* O, float* L, i
  * The same with modified scores, as in fa_fwd_ranges below (fa_fwd_tree is softcap = 0 and slopes = NULL):
  *   softcap : 0 for none, else 1e-3 .. 1e3 (outside: FA_ERR_UNSUPPORTED): the scaled score s
  *             becomes softcap tanh(s / softcap)
- *   slopes  : fp32 [H] device array of finite numbers, or NULL: token t, at position
+ *   slopes  : fp32 [H] device array, or NULL, in size as there: token t, at position
  *             lens[b] - n_new[b] + t, takes slopes[h] times the distance from row j off its
  *             score.  Needs tree = NULL (FA_ERR_UNSUPPORTED): in a tree a token's position is not its row.
  */
@@ -377,11 +377,12 @@ fa_status fa_fwd_tree_ex(const void* Q, const fa_cache* cache, void* O, float* L
  * A mask says for each query row i of sequence b which keys it sees: first <= j < last,
  * one range for all heads.  Documents packed into a sequence, padding, prefixes that see
  * one another, causal masks and windows all are of this kind.  It lies in a buffer of
- * fa_mask_size() bytes ((size_t)-1: sizes that are refused) that the caller owns: int32 first [B,Nq], then last
- * [B,Nq] (each padded to 16 bytes; both 0 for a row that sees no key), then tables of
- * the call's own.  The calls below read the buffer only; nothing but the two makers may
- * write it.  One mask serves any number of calls, at the same time too.  B <= 65535,
- * B*Nq and B*Nk < 2^31, Nq and Nk <= 2^30.  mask: 16-byte aligned; smaller or missing: FA_ERR_WORKSPACE.
+ * fa_mask_size() bytes ((size_t)-1: sizes that are refused) that the caller owns: int32
+ * first [B,Nq], then last [B,Nq] (each padded to 16 bytes; both 0 for a row that sees no
+ * key), then tables of the call's own.  The calls below read the buffer only, and take it
+ * for the mask of their B, Nq and Nk; nothing but the two makers may write it.  One mask
+ * serves any number of calls, at the same time too.  B <= 65535, B*Nq and B*Nk < 2^31, Nq
+ * and Nk <= 2^30.  mask: 16-byte aligned; smaller or missing: FA_ERR_WORKSPACE.
  * ---------------------------------------------------------------------------
  */
 size_t fa_mask_size(int B, int Nq, int Nk);
@@ -415,7 +416,7 @@ fa_status fa_mask_from_ranges(void* mask, size_t mask_bytes, int B, int Nq, int 
  *       reads key head h / (H / Hk)
  *   O : out, bf16 contiguous [B,H,Nq,d];  L : out, fp32 [B,H,Nq]
  *   softcap : 0 for none, else 1e-3 .. 1e3 (outside: FA_ERR_UNSUPPORTED)
- *   slopes  : fp32 [H] device array of finite numbers, or NULL
+ *   slopes  : fp32 [H] device array, or NULL; slopes[h] (Nq + Nk) below 2^100 in size
  * A row that sees no key gets O = 0 and L = -infinity.  Keys a row does not see never
  * reach it, be their keys or values infinite or NaN.  An infinite or NaN value that a row
  * sees makes that element of its output infinite or NaN.
@@ -434,10 +435,12 @@ fa_status fa_fwd_ranges(const void* Q, const void* K, const void* V, void* O, fl
  * Rows that see no key and keys that no row sees get zero gradients and may hold anything:
  * nothing of them (nor of their dO) reaches the other gradients.  An infinite or NaN key that
  * rows see makes its dK and dV and those rows' dQ NaN (and, where L is NaN, the gradients of
- * what these rows see).  (An infinity or NaN in a row of Q or dO, or in a value, that takes part
- * makes gradients NaN, also of keys and rows near it that it does not see.)  dQ's sums over key tiles are fp32 additions in no fixed order; dK and dV are the
- * same on every run.  They add up in the tensor cores, which cut each term below 2^-25 of the
- * sum: n terms (rows times query heads) of one sign and size are off by up to n 2^-26 of it.  Slopes are constants: they have no gradient.
+ * what these rows see).  An infinity or NaN in a row of Q or dO, or in a value, that takes part
+ * makes gradients NaN, also of keys and rows near it that it does not see.  dQ's sums over key
+ * tiles are fp32 additions in no fixed order; dK and dV are the same on every run.  These add
+ * up in the tensor cores, which cut each term below 2^-25 of the sum: n terms (rows times
+ * query heads) of one sign and size are off by up to n 2^-26 of it.  Slopes are constants:
+ * they have no gradient.
  */
 size_t fa_bwd_ranges_workspace_size(int B, int H, int Hk, int Nq, int Nk, int d);
 fa_status fa_bwd_ranges(const void* Q, const void* K, const void* V, const void* O, const void* dO, const float* L,
