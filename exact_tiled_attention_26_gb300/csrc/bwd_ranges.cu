@@ -81,6 +81,11 @@ struct BwdRangesArgs {
   int* status;
 };
 
+// Sums times their scale.  (0 stays +0 with a negative one.)
+FA_DEV uint32_t scaled_bf16x2(float x, float y, float scale) {
+  return pack_bf16x2(fmaf(x, scale, 0.f), fmaf(y, scale, 0.f));
+}
+
 FA_DEV Stage* stage_of(const Ctx& x, int g) { return reinterpret_cast<Stage*>(x.small + ROFF_STAGE) + (g & 1); }
 
 // Producer (whole warp): Q, dO of query tile i of head h into stage g % 2, and the tile's Stage.
@@ -763,7 +768,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           }
           const float f = is_k ? a.scale : 1.f;
 #pragma unroll
-          for (int e = 0; e < 16; ++e) o[e] = pack_bf16x2(__uint_as_float(r[2 * e]) * f, __uint_as_float(r[2 * e + 1]) * f);
+          for (int e = 0; e < 16; ++e) o[e] = scaled_bf16x2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]), f);
           if (DR == D || h == 0)  // (d = 32: the other half is padding)
             warp_store_rows<4, 0>(o, reinterpret_cast<uint8_t*>((is_k ? a.dK : a.dV) + krow0 * DR + (DR == D ? col : 0)),
                                   DR * 2, m.Nk - row0, lane);
@@ -850,7 +855,7 @@ __global__ void __launch_bounds__(256) bwd_ranges_finish(const __grid_constant__
       for (int k = 1; k < kParts; ++k) x[0].x += x[k].x, x[0].y += x[k].y, x[0].z += x[k].z, x[0].w += x[k].w;
       const float f = t == 0 ? a.scale : 1.f;
       *reinterpret_cast<uint2*>((t == 0 ? a.dK : a.dV) + (out0 + row) * DR + col) =
-          make_uint2(pack_bf16x2(x[0].x * f, x[0].y * f), pack_bf16x2(x[0].z * f, x[0].w * f));
+          make_uint2(scaled_bf16x2(x[0].x, x[0].y, f), scaled_bf16x2(x[0].z, x[0].w, f));
     }
     return;
   }
@@ -858,8 +863,8 @@ __global__ void __launch_bounds__(256) bwd_ranges_finish(const __grid_constant__
   for (long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; i < n8; i += step) {
     const float4 x = __ldcs(reinterpret_cast<const float4*>(a.dQacc + 8 * i)), y = __ldcs(reinterpret_cast<const float4*>(a.dQacc + 8 * i + 4));
     *reinterpret_cast<uint4*>(dQ + 8 * i) =
-        make_uint4(pack_bf16x2(x.x * a.scale, x.y * a.scale), pack_bf16x2(x.z * a.scale, x.w * a.scale),
-                   pack_bf16x2(y.x * a.scale, y.y * a.scale), pack_bf16x2(y.z * a.scale, y.w * a.scale));
+        make_uint4(scaled_bf16x2(x.x, x.y, a.scale), scaled_bf16x2(x.z, x.w, a.scale),
+                   scaled_bf16x2(y.x, y.y, a.scale), scaled_bf16x2(y.z, y.w, a.scale));
   }
 }
 

@@ -88,6 +88,18 @@ def test_no_query_rows_give_keys_no_gradients(fa_lib, B, H, Hk, Nq, Nk, d):
     clean_status(fa)
 
 
+@pytest.mark.parametrize("d,cap", [(128, 0.0), (128, 20.0), (64, 20.0), (32, 20.0)])
+def test_zero_gradients_are_positive_zeros(fa_lib, d, cap):
+    """Padding (rows without keys, keys that no row sees), in tiles with others and in tiles of its own."""
+    fa = fa_lib
+    g = torch.Generator().manual_seed(3)
+    q, k, v, do = (rand(g, 2, h, 700, d) for h in (4, 2, 2, 4))
+    m = fa.mask_ranges(2, 700, causal=True, documents=i32([[0, 700], [0, 300]]))
+    o, lse = fa.attention_ranges(q, k, v, m, softcap=cap)
+    for x in fa.attention_ranges_backward(q, k, v, o, lse, do, m, softcap=cap):
+        assert not x[1, :, 300:].contiguous().view(torch.int16).any()
+
+
 # ------------------------------------------------------------------ scores far beyond the cap
 
 @pytest.mark.parametrize("d,bias", [(32, False), (64, True), (128, False)])
