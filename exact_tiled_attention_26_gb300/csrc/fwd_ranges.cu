@@ -20,7 +20,7 @@
 // product's burst; 0.86 us a tile pair): issue of the two softmax warps of a scheduler, and shared memory's port, which
 // the products' operands and the loads share.  With one warp for a row's 128 scores the same took 1.71 ms.  With a cap the
 // special-function unit (ranges_score.cuh), with a bias the issue slots again (2.07 ms).  Short documents (2 x 4096 tokens,
-// 7 documents each, 16 + 4 heads: 41.6 us, 25 of them the tile pairs at that rate): the units' borders, and instruction
+// 7 documents each, 16 + 4 heads: 42.0 us, 25 of them the tile pairs at that rate): the units' borders, and instruction
 // fetches.  The roles of a CTA run code of their own all the time, and what does not fit the instruction caches comes from
 // one that several SMs share: with 130 KB of code its request rate was at 0.77 of its peak and the same call took 62 us
 // (now 70 KB).  So masked and whole tiles run the same code, and what runs once a unit, and the issue of the products, is a
